@@ -335,6 +335,95 @@ int moe_qk_norm_rope(uint16_t* qkv, int T, int num_q_heads, int num_kv_heads, in
  * computed in float64 and rounded to float32. rotary_dim even, theta > 1. */
 int moe_rope_cos_sin_table(float* cos_sin, int max_pos, int rotary_dim, double theta, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged key/value cache behind that step, and the attention that reads it.
+ *
+ * Cache: k_cache and v_cache are arrays of num_pages pages, page_stride ELEMENTS apart
+ * (so keys and values may share one allocation, page by page); a page holds
+ * [num_kv_heads][page_size][head_dim] elements, the tokens of one kv head side by side.
+ *   kv_type SRMOE_KV_BF16: bf16 elements; k_scale / v_scale are not read.
+ *   kv_type SRMOE_KV_E4M3: e4m3 bytes c that stand for c * scale[kv head]; k_scale, v_scale
+ *           [num_kv_heads] float32, positive and finite.
+ * A cache slot is page * page_size + offset. Offsets inside the cache are 64-bit.
+ *   limits: head_dim in {64, 128, 256}; page_size a power of two in 16..1024; 1 <=
+ *   num_pages, num_pages * page_size < 2^31; page_stride >= num_kv_heads * page_size *
+ *   head_dim and a multiple of 16.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  SRMOE_KV_BF16 = 0,
+  SRMOE_KV_E4M3 = 1
+} srmoe_kv_type;
+
+/* moe_kv_append: moe_qk_norm_rope (fused form) that leaves qkv as it is and writes the
+ * rotated q heads to q_out and the rotated k heads and the v heads into the cache.
+ *   qkv        rows of (num_q_heads + 2*num_kv_heads) * head_dim bf16 values, qkv_stride
+ *              values apart (>= that row, a multiple of 8)
+ *   rotary_dim as for moe_qk_norm_rope, or 0: no rotation (positions, cos_sin not read)
+ *   q_norm_w, k_norm_w: as there, or BOTH NULL: no norm
+ *   slots      [T] int32: token t's k and v go to slot slots[t]; a token whose slot is
+ *              outside [0, num_pages * page_size) (-1 for padding) is not cached. Two tokens
+ *              with the same slot leave that slot's bytes undefined (and no others).
+ *   q_out      [T, num_q_heads, head_dim] bf16 out, written for every token (NULL when
+ *              num_q_heads == 0)
+ *   Float32 arithmetic and one rounding per value: bf16 (to nearest even), or e4m3 of
+ *   value / scale (to nearest even, saturating at +-448; NaN stays NaN).
+ *   limits: num_kv_heads >= 1, and those of moe_qk_norm_rope and of the cache. */
+int moe_kv_append(const uint16_t* qkv, size_t qkv_stride, int T, int num_q_heads, int num_kv_heads, int head_dim,
+                  int rotary_dim, int neox, const float* q_norm_w, const float* k_norm_w, float eps,
+                  const int32_t* positions, const float* cos_sin, int max_pos, const int32_t* slots,
+                  uint16_t* q_out, void* k_cache, void* v_cache, int kv_type, const float* k_scale,
+                  const float* v_scale, int num_pages, int page_size, size_t page_stride, void* stream);
+
+/* Attention of S sequences' query tokens over their cached tokens. For query head h of
+ * token r (kv head h / (num_q_heads / num_kv_heads)), over the cached tokens j it sees:
+ *     z_j = scale * q_r.k_j, or softcap * tanh(scale * q_r.k_j / softcap) when softcap > 0
+ *     lse[r,h] = log sum_j exp(z_j)      out[r,h,:] = sum_j exp(z_j - lse[r,h]) v_j
+ * A row that sees nothing gets out = 0 and lse = -infinity.
+ *   q           token r's heads [num_q_heads, head_dim] bf16 at q + r * q_stride (q_stride >=
+ *               num_q_heads * head_dim, a multiple of 8): q_out of moe_kv_append, or the
+ *               q heads of a qkv row
+ *   block_table [S, max_pages] int32: sequence s's token j lies in page block_table[s, j /
+ *               page_size], offset j % page_size. Only the entries of tokens below kv_lens[s]
+ *               are read. Tokens of a page outside [0, num_pages) are seen by nobody.
+ *   cu_q        [S+1] int32, ascending: tokens cu_q[s]..cu_q[s+1]-1 of q are sequence s's, n_s of
+ *               them, at most max_q (further ones are not computed). Rows of out and lse
+ *               outside every sequence are left as they were.
+ *   kv_lens     [S] int32: cached tokens of the sequence, its n_s query tokens being the last
+ *               of them (append first); at most max_pages * page_size count. What the cache
+ *               holds past them is never used, whatever it is (NaN included); the
+ *               cached tokens before must be finite.
+ *   out         [T, num_q_heads, head_dim] bf16;  lse [T, num_q_heads] float32, or NULL
+ *   workspace   >= moe_attention_workspace_bytes(...) bytes, device; calls that may overlap in
+ *               time need one each. Nothing in it needs to start at zero.
+ * moe_tree_attention: drafted tokens. Query token i of sequence s is cached token ctx + i,
+ *   ctx = kv_lens[s] - n_s. It sees every token below ctx, and token ctx + b when bit b of its
+ *   tree_mask word is set (b < n_s; its own bit included: a token that sees itself has it
+ *   set). tree_mask [T] uint64, or NULL: token i sees ctx..ctx + i (a chain; with one token per
+ *   sequence, ordinary decoding). max_q <= 64.
+ * moe_prefill_attention: a chunk of a prompt. Token i sees the cached tokens j <= ctx + i, and
+ *   those j < prefix_lens[s] (prefix_lens [S] int32, or NULL: none), j < kv_lens[s].
+ *   Scores, softmax statistics and sums are float32. The weights exp(z - max) that multiply v
+ *   are rounded to the matrix cores' type: bf16 (2^-9 relative, as the output's own
+ *   rounding), float16 for an e4m3 cache (2^-12); lse sums the unrounded ones.
+ *   limits: those of the cache; num_q_heads a multiple of num_kv_heads, at most 128 times
+ *   it, num_q_heads <= 1024; S <= 65536; max_pages * page_size < 2^30; scale > 0;
+ *   softcap >= 0.
+ * Results do not depend on scheduling: no atomics, sums in a fixed order. */
+int moe_tree_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
+                       const float* k_scale, const float* v_scale, int num_pages, int page_size,
+                       size_t page_stride, const int32_t* block_table, int max_pages, const int32_t* cu_q,
+                       const int32_t* kv_lens, const uint64_t* tree_mask, int S, int T, int max_q,
+                       int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap, uint16_t* out,
+                       float* lse, void* workspace, size_t ws_bytes, void* stream);
+int moe_prefill_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
+                          const float* k_scale, const float* v_scale, int num_pages, int page_size,
+                          size_t page_stride, const int32_t* block_table, int max_pages, const int32_t* cu_q,
+                          const int32_t* kv_lens, const int32_t* prefix_lens, int S, int T, int max_q,
+                          int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap,
+                          uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+/* Bytes of workspace for either call (host; 0 for sizes that they refuse). */
+size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim);
+
 /* Host helpers. */
 size_t moe_sorted_capacity(int T, int K1, int E1, int block_m); /* P_max, rows */
 size_t moe_align_workspace_bytes(int T, int K1, int E1);

@@ -42,3 +42,4 @@ __all__ = ["qk_norm_rope", "head_rms_norm", "rope_half", "rope_interleaved", "ro
            "align_by_expert", "sorted_capacity", "quantize_act", "dequant_weight",
            "expert_ffn", "moe_unfused", "moe_fused", "slot_outputs", "combine_slots",
            "dense_shared_ffn"]
+from .kv import attend, visible_tree, visible_prefill

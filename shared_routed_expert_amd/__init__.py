@@ -14,8 +14,10 @@ _BINDING = ("lib", "LIB_PATH", "SrmoeError", "SCALE_PER_CHANNEL", "SCALE_BLOCK12
             "moe_ffn_workspace_bytes", "moe_ffn_workspace_offsets", "moe_qk_norm_rope", "moe_rope_cos_sin_table",
             "moe_route_from_x", "moe_route_from_x_workspace_bytes", "moe_layer_forward_from_x",
             "moe_workspace_bytes", "moe_status_string", "moe_layer_forward_staged",
-            "moe_layer_forward_noalloc", "NOALLOC_SCRATCH_BYTES")
+            "moe_layer_forward_noalloc", "NOALLOC_SCRATCH_BYTES", "KV_BF16", "KV_E4M3", "moe_kv_append",
+            "moe_tree_attention", "moe_prefill_attention", "moe_attention_workspace_bytes")
 _LAYER = ("FusedMoE", "UnfusedMoE", "DeviceWeights")
+_CACHE = ("PagedKVCache",)
 
 
 def __getattr__(name):
@@ -25,4 +27,7 @@ def __getattr__(name):
     if name in _LAYER:
         from . import layer
         return getattr(layer, name)
+    if name in _CACHE:
+        from . import cache
+        return getattr(cache, name)
     raise AttributeError(name)

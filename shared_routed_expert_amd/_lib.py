@@ -17,6 +17,8 @@ LIB_PATH = os.path.join(_PKG, "libsrmoe.so")
 SRMOE_OK = 0
 SCALE_PER_CHANNEL = 0
 SCALE_BLOCK128 = 1
+KV_BF16 = 0
+KV_E4M3 = 1
 
 
 class SrmoeError(RuntimeError):
@@ -57,6 +59,11 @@ def _load():
         "moe_route_from_x_workspace_bytes": ([I, I, I], Z),
         "moe_layer_forward_from_x": ([P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, P, P, P, P, P, P, P, P, Z, P, Z,
                                       P, Z, P, P], I),
+        "moe_kv_append": ([P, Z, I, I, I, I, I, I, P, P, F, P, P, I, P, P, P, P, I, P, P, I, I, Z, P], I),
+        "moe_tree_attention": ([P, Z, P, P, I, P, P, I, I, Z, P, I, P, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P], I),
+        "moe_prefill_attention": ([P, Z, P, P, I, P, P, I, I, Z, P, I, P, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P],
+                                  I),
+        "moe_attention_workspace_bytes": ([I, I, I, I, I, I], Z),
         "moe_rope_cos_sin_table": ([P, I, I, ctypes.c_double, P], I),
         "moe_sorted_capacity": ([I, I, I, I], Z),
         "moe_align_workspace_bytes": ([I, I, I], Z),
@@ -87,7 +94,8 @@ EXPORTED = ("moe_route_topk_plus_shared", "moe_align_by_expert", "moe_fused_ffn"
             "moe_route_from_x_workspace_bytes", "moe_layer_forward_from_x", "moe_sorted_capacity",
             "moe_align_workspace_bytes", "moe_ffn_workspace_bytes", "moe_ffn_workspace_offsets",
             "srmoe_status_string", "srmoe_last_hip_error", "moe_workspace_bytes", "moe_status_string",
-            "moe_layer_forward_staged", "moe_layer_forward_noalloc", "srmoe_source_hash")
+            "moe_layer_forward_staged", "moe_layer_forward_noalloc", "srmoe_source_hash", "moe_kv_append",
+            "moe_tree_attention", "moe_prefill_attention", "moe_attention_workspace_bytes")
 
 
 def _ptr(t):
@@ -303,3 +311,38 @@ def moe_layer_forward_from_x(x, w_router, bias, w13, s13, w2, s2, scale_mode, T,
         _ptr(expert_counts), _ptr(expert_offsets), _ptr(num_padded), _ptr(router_ws), router_ws_bytes,
         _ptr(align_ws), align_ws_bytes, _ptr(ffn_ws), ffn_ws_bytes, _ptr(out), _stream(stream))
     return _check("moe_layer_forward_from_x", st) if check else st
+
+
+def moe_kv_append(qkv, qkv_stride, T, num_q_heads, num_kv_heads, head_dim, rotary_dim, neox, q_norm_w, k_norm_w, eps,
+                  positions, cos_sin, max_pos, slots, q_out, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages,
+                  page_size, page_stride, stream=None, check=True):
+    st = lib.moe_kv_append(_ptr(qkv), qkv_stride, T, num_q_heads, num_kv_heads, head_dim, rotary_dim, int(neox),
+                           _ptr(q_norm_w), _ptr(k_norm_w), eps, _ptr(positions), _ptr(cos_sin), max_pos, _ptr(slots),
+                           _ptr(q_out), _ptr(k_cache), _ptr(v_cache), kv_type, _ptr(k_scale), _ptr(v_scale), num_pages,
+                           page_size, page_stride, _stream(stream))
+    return _check("moe_kv_append", st) if check else st
+
+
+def moe_attention_workspace_bytes(S, T, max_q, num_q_heads, num_kv_heads, head_dim):
+    return lib.moe_attention_workspace_bytes(S, T, max_q, num_q_heads, num_kv_heads, head_dim)
+
+
+def moe_tree_attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
+                       block_table, max_pages, cu_q, kv_lens, tree_mask, S, T, max_q, num_q_heads, num_kv_heads,
+                       head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream=None, check=True):
+    st = lib.moe_tree_attention(_ptr(q), q_stride, _ptr(k_cache), _ptr(v_cache), kv_type, _ptr(k_scale), _ptr(v_scale),
+                                num_pages, page_size, page_stride, _ptr(block_table), max_pages, _ptr(cu_q),
+                                _ptr(kv_lens), _ptr(tree_mask), S, T, max_q, num_q_heads, num_kv_heads, head_dim,
+                                scale, softcap, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
+    return _check("moe_tree_attention", st) if check else st
+
+
+def moe_prefill_attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
+                          block_table, max_pages, cu_q, kv_lens, prefix_lens, S, T, max_q, num_q_heads, num_kv_heads,
+                          head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream=None, check=True):
+    st = lib.moe_prefill_attention(_ptr(q), q_stride, _ptr(k_cache), _ptr(v_cache), kv_type, _ptr(k_scale),
+                                   _ptr(v_scale), num_pages, page_size, page_stride, _ptr(block_table), max_pages,
+                                   _ptr(cu_q), _ptr(kv_lens), _ptr(prefix_lens), S, T, max_q, num_q_heads,
+                                   num_kv_heads, head_dim, scale, softcap, _ptr(out), _ptr(lse), _ptr(workspace),
+                                   ws_bytes, _stream(stream))
+    return _check("moe_prefill_attention", st) if check else st

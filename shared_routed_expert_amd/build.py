@@ -23,7 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsrmoe.so")
 SOURCES = ["api.hip", "router.hip", "route.hip", "align.hip", "quant.hip", "ffn.hip", "ffn_decode.hip",
-           "ffn_expert_decode.hip", "ffn_tile.hip", "front.hip", "qknorm.hip"]
+           "ffn_expert_decode.hip", "ffn_tile.hip", "front.hip", "qknorm.hip",
+           "kv_append.hip", "attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

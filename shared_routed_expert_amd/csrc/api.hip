@@ -5,6 +5,7 @@
 #include <functional>
 #include <mutex>
 
+#include "attention.hpp"
 #include "front_dev.hpp"
 
 namespace srmoe {
@@ -53,6 +54,7 @@ hipError_t launch_expert_ffn_decode(const uint8_t*, const float*, const uint8_t*
 hipError_t launch_qk_norm_rope(uint16_t*, int, int, int, int, int, bool, const float*, const float*, float,
                                const int32_t*, const float*, int, bool, hipStream_t);
 hipError_t launch_rope_table(float*, int, int, double, hipStream_t);
+hipError_t launch_kv_append(const KvAppendArgs&, hipStream_t);
 }  // namespace srmoe
 
 using namespace srmoe;
@@ -739,6 +741,135 @@ int moe_qk_norm_rope(uint16_t* qkv, int T, int num_q_heads, int num_kv_heads, in
   return hip_status(launch_qk_norm_rope(qkv, T, num_q_heads, num_kv_heads, head_dim, rotary_dim, neox != 0,
                                         q_norm_w, k_norm_w, eps, positions, cos_sin, max_pos, fused != 0,
                                         as_stream(stream)));
+}
+
+// ---------------------------------------------------------------------------------------
+// Paged cache and attention
+
+// Shape checks of the cache, shared by the calls that write and read it.
+static int check_cache_dims(int kv_type, int num_kv_heads, int head_dim, int num_pages, int page_size,
+                            size_t page_stride) {
+  if (num_kv_heads < 1 || num_pages < 1 || (kv_type != SRMOE_KV_BF16 && kv_type != SRMOE_KV_E4M3))
+    return SRMOE_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return SRMOE_ERR_UNSUPPORTED;
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return SRMOE_ERR_UNSUPPORTED;
+  if ((size_t)num_pages * page_size >= ((size_t)1 << 31) || num_kv_heads > 1024) return SRMOE_ERR_UNSUPPORTED;
+  if (page_stride < (size_t)num_kv_heads * page_size * head_dim || page_stride % 16 != 0 ||
+      page_stride >= ((size_t)1 << 40))
+    return SRMOE_ERR_INVALID_ARG;
+  return SRMOE_OK;
+}
+
+int moe_kv_append(const uint16_t* qkv, size_t qkv_stride, int T, int num_q_heads, int num_kv_heads, int head_dim,
+                  int rotary_dim, int neox, const float* q_norm_w, const float* k_norm_w, float eps,
+                  const int32_t* positions, const float* cos_sin, int max_pos, const int32_t* slots,
+                  uint16_t* q_out, void* k_cache, void* v_cache, int kv_type, const float* k_scale,
+                  const float* v_scale, int num_pages, int page_size, size_t page_stride, void* stream) {
+  if (T < 0 || T > kMaxT || num_q_heads < 0 || !(eps >= 0.f) || !(eps < 1e30f)) return SRMOE_ERR_INVALID_ARG;
+  const int st = check_cache_dims(kv_type, num_kv_heads, head_dim, num_pages, page_size, page_stride);
+  if (st != SRMOE_OK) return st;
+  if (num_q_heads > 1024 || num_q_heads + 2 * num_kv_heads > 1024) return SRMOE_ERR_UNSUPPORTED;
+  if (rotary_dim != 0) {
+    if (!qk_dims_supported(head_dim, rotary_dim)) return SRMOE_ERR_UNSUPPORTED;
+    if (max_pos < 1) return SRMOE_ERR_INVALID_ARG;
+    if ((size_t)max_pos * rotary_dim >= ((size_t)1 << 31)) return SRMOE_ERR_UNSUPPORTED;
+  }
+  if (qkv_stride < (size_t)(num_q_heads + 2 * num_kv_heads) * head_dim || qkv_stride % 8 != 0 ||
+      qkv_stride >= ((size_t)1 << 40))
+    return SRMOE_ERR_INVALID_ARG;
+  if (T == 0) return SRMOE_OK;
+  const bool norm = q_norm_w || k_norm_w;
+  if (norm && ((num_q_heads > 0 && !q_norm_w) || !k_norm_w)) return SRMOE_ERR_INVALID_ARG;
+  if (!qkv || !slots || !k_cache || !v_cache || (num_q_heads > 0 && !q_out)) return SRMOE_ERR_INVALID_ARG;
+  if (rotary_dim != 0 && (!positions || !cos_sin)) return SRMOE_ERR_INVALID_ARG;
+  if (kv_type == SRMOE_KV_E4M3 && (!k_scale || !v_scale)) return SRMOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {qkv, q_norm_w, k_norm_w, positions, cos_sin, slots, q_out, k_cache, v_cache, k_scale, v_scale};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
+  KvAppendArgs a{};
+  a.qkv = qkv; a.qkv_stride = qkv_stride; a.T = T; a.Hq = num_q_heads; a.Hkv = num_kv_heads; a.D = head_dim;
+  a.rd = rotary_dim; a.neox = neox != 0; a.norm = norm; a.qw = q_norm_w; a.kw = k_norm_w; a.eps = eps;
+  a.positions = positions; a.cos_sin = cos_sin; a.max_pos = max_pos; a.slots = slots; a.q_out = q_out;
+  a.k_cache = k_cache; a.v_cache = v_cache; a.fp8 = kv_type == SRMOE_KV_E4M3; a.k_scale = k_scale;
+  a.v_scale = v_scale; a.num_slots = num_pages * page_size; a.page_stride = page_stride;
+  a.page_shift = __builtin_ctz((unsigned)page_size);
+  return hip_status(launch_kv_append(a, as_stream(stream)));
+}
+
+// Sizes that both attention calls share; 0 if fine.
+static int check_attention_dims(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim) {
+  if (S < 0 || T < 0 || T > kMaxT || max_q < 1 || num_q_heads < 1 || num_kv_heads < 1) return SRMOE_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return SRMOE_ERR_UNSUPPORTED;
+  if (num_q_heads % num_kv_heads != 0) return SRMOE_ERR_INVALID_ARG;
+  if (num_q_heads > 1024 || num_q_heads / num_kv_heads > 128 || S > 65536 || max_q > kMaxT)
+    return SRMOE_ERR_UNSUPPORTED;
+  return SRMOE_OK;
+}
+
+size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim) {
+  if (check_attention_dims(S, T, max_q, num_q_heads, num_kv_heads, head_dim) != SRMOE_OK) return 0;
+  const size_t n = attention_workspace_bytes(S, max_q, num_q_heads, num_kv_heads, head_dim);
+  return n > 256 ? n : 256;
+}
+
+static int attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
+                     const float* k_scale, const float* v_scale, int num_pages, int page_size, size_t page_stride,
+                     const int32_t* block_table, int max_pages, const int32_t* cu_q, const int32_t* kv_lens,
+                     const uint64_t* tree_mask, const int32_t* prefix_lens, int S, int T, int max_q,
+                     int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap, uint16_t* out,
+                     float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  int st = check_attention_dims(S, T, max_q, num_q_heads, num_kv_heads, head_dim);
+  if (st != SRMOE_OK) return st;
+  st = check_cache_dims(kv_type, num_kv_heads, head_dim, num_pages, page_size, page_stride);
+  if (st != SRMOE_OK) return st;
+  if (max_pages < 1 || !(scale > 0.f) || !(scale < 1e30f) || !(softcap >= 0.f) || !(softcap < 1e30f))
+    return SRMOE_ERR_INVALID_ARG;
+  if ((size_t)max_pages * page_size >= ((size_t)1 << 30)) return SRMOE_ERR_UNSUPPORTED;
+  if (q_stride < (size_t)num_q_heads * head_dim || q_stride % 8 != 0 || q_stride >= ((size_t)1 << 40))
+    return SRMOE_ERR_INVALID_ARG;
+  if (T == 0 || S == 0) return SRMOE_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !cu_q || !kv_lens || !out || !workspace)
+    return SRMOE_ERR_INVALID_ARG;
+  if (kv_type == SRMOE_KV_E4M3 && (!k_scale || !v_scale)) return SRMOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, tree_mask, prefix_lens, out,
+                        lse, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_attention_workspace_bytes(S, T, max_q, num_q_heads, num_kv_heads, head_dim))
+    return SRMOE_ERR_WORKSPACE;
+  AttnArgs a{};
+  a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_scale = kv_type == SRMOE_KV_E4M3 ? k_scale : nullptr;
+  a.v_scale = kv_type == SRMOE_KV_E4M3 ? v_scale : nullptr;
+  a.num_pages = num_pages; a.page_shift = __builtin_ctz((unsigned)page_size); a.page_stride = page_stride;
+  a.block_table = block_table; a.max_pages = max_pages; a.cu_q = cu_q; a.kv_lens = kv_lens;
+  a.tree_mask = tree_mask; a.prefix_lens = prefix_lens; a.S = S; a.T = T; a.max_q = max_q; a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads; a.G = num_q_heads / num_kv_heads; a.D = head_dim; a.scale = scale; a.softcap = softcap;
+  a.out = out; a.lse = lse; a.ws = workspace;
+  return hip_status(launch_attention(a, as_stream(stream)));
+}
+
+int moe_tree_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
+                       const float* k_scale, const float* v_scale, int num_pages, int page_size,
+                       size_t page_stride, const int32_t* block_table, int max_pages, const int32_t* cu_q,
+                       const int32_t* kv_lens, const uint64_t* tree_mask, int S, int T, int max_q,
+                       int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap, uint16_t* out,
+                       float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  if (max_q > 64) return SRMOE_ERR_UNSUPPORTED;   // a token's mask is one 64-bit word
+  return attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
+                   block_table, max_pages, cu_q, kv_lens, tree_mask, nullptr, S, T, max_q, num_q_heads,
+                   num_kv_heads, head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream);
+}
+
+int moe_prefill_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
+                          const float* k_scale, const float* v_scale, int num_pages, int page_size,
+                          size_t page_stride, const int32_t* block_table, int max_pages, const int32_t* cu_q,
+                          const int32_t* kv_lens, const int32_t* prefix_lens, int S, int T, int max_q,
+                          int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap,
+                          uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
+                   block_table, max_pages, cu_q, kv_lens, nullptr, prefix_lens, S, T, max_q, num_q_heads,
+                   num_kv_heads, head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"
