@@ -1,111 +1,797 @@
-// Attention over the paged cache, in its plainest form: one wavefront per query head of
-// a token walks the sequence's keys 64 at a time, a key per lane for the scores and D / 64
-// dims per lane for the weighted values, with the running maximum m and sum l of the
-// softmax (float32):
-//     m' = max(m, max z),  l' = l e^(m - m') + sum e^(z - m'),  o' = o e^(m - m') + sum e^(z - m') v
+// Attention over the paged cache on the matrix cores, for drafted trees, single tokens and
+// prompt chunks alike.
+//
+// Rows. The query heads that share a kv head read the same keys, so a tile's rows are (token,
+// head of the group) pairs: TB = M / G tokens of a sequence times its G heads, M = 32 QT RW rows.
+// A segment is one such tile against all keys it sees. Row r of a tile sees key j when j <
+// lim_r, or when j is a drafted token whose bit is set in the row's mask word; causal order, a
+// prefix and a tree are all of this form.
+//
+// Products. Scores are taken transposed, S^T = K Q^T (32x32x16 matrix instructions): a lane then
+// owns one row (its column l & 31) and 16 keys per 32x32 tile, so the running maximum and sum
+// of the softmax are sums in registers plus one exchange with lane l ^ 32, and a change of the
+// maximum scales O^T by one number per lane. The weights, rounded to 16 bits, are already the B
+// operand of O^T += V^T P^T when the keys of a 16-key step are counted as (half h of the wave,
+// j < 8) -> key 8 (j / 4) + 4 h + j % 4; V's transposing LDS reads fetch them in that order.
+//   m' = max(m, max z),  O' = O 2^(m - m') + sum 2^(z - m') v,  l' = l 2^(m - m') + sum 2^(z - m')
+// (z in units of log2 e). m only moves when a score exceeds it by more than 2^8: until then
+// the weights are at most 2^8, which float32 sums and both 16-bit types hold.
+//
+// Keys and values go to LDS straight from global memory (16 bytes a lane), 16-byte chunks swapped
+// within a row by the source address (chunk c of key k sits at c ^ swizzle(k)), so that both
+// the row-wise reads of K and the transposing reads of V use all banks.
+//
+// Two arrangements of a workgroup's waves:
+//   RW == 1 (decode, small trees): every wave walks keys of its own through its own two LDS
+//     stages, with no barrier; the KW waves' sums are joined at the end of the segment.
+//   KW == 1 (larger trees, prompts): RW waves with rows of their own share each key tile.
+//
+// Work split. The segments of all sequences, heads and row tiles are laid end to end, each as
+// long as the keys it sees; workgroup w takes the w-th of equal parts of that line, so ragged
+// batches and causal triangles balance without a host-side plan. A segment that spans several
+// parts leaves one partial (O, m, l) per part in the workspace, joined by a second kernel in
+// part order (no atomics; the same bits every time).
 #include "attention.hpp"
 #include "common.hpp"
 
 namespace srmoe {
 
-__device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
-  return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kMoveMax = 8.0f;    // a running maximum moves when a score exceeds it by this (base 2)
+constexpr int kSegCost = 64;        // a segment's fixed cost, in keys, for the work split
+constexpr int kMinPart = 256;       // a part holds at least this many keys' cost
+
+// 16-byte chunk swap of key k's row (CPR chunks): distinct for 8 consecutive keys (reads of K) and
+// for {4h..4h+3, 8+4h..8+4h+3} of 16 keys (transposing reads of V).
+__device__ __forceinline__ int swizzle(int k, int cpr) {
+  return (((k & 3) << 1) | (((k >> 2) ^ (k >> 3)) & 1)) & (cpr - 1);
 }
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(64) attention_plain_kernel(const AttnArgs a) {
-  __shared__ float qs[D];
-  __shared__ float ps[kWave];
-  __shared__ long base[kWave];
-  const int lane = threadIdx.x, h = blockIdx.y, hk = h / a.G;
-  // sequence of query row blockIdx.x
-  const int row = blockIdx.x;
-  int s = -1;
-  SeqInfo si{};
-  for (int i = 0; i < a.S; ++i) {
-    si = seq_info(a, i);
-    if (row >= si.row0 && row < si.row0 + si.n) {
-      s = i;
-      break;
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float swap_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float swap_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ long uni(long v) {
+  const uint32_t lo = (uint32_t)uni((int)(uint32_t)v), hi = (uint32_t)uni((int)(uint32_t)((uint64_t)v >> 32));
+  return (long)(((uint64_t)hi << 32) | lo);
+}
+
+// 16 bytes per lane from base + voff to LDS address `lds` + 16 * lane. In asm, because the
+// compiler would wait for every such load in flight before any later LDS read; wait_vm counts them.
+__device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t voff, const uint8_t* base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uni((int)lds)), "v"(voff),
+               "s"(uni((long)base))
+               : "memory");
+}
+
+// ------------------------------------------------------------------------------- the work split
+// One sequence's row tiles: tile i (of MT) sees the first vis(i) = max(lo, ctx + min(n, (i + 1) TB))
+// keys (lo: what every row may see at least: its prefix, or all keys under a tree mask).
+struct SeqTiles {
+  int row0, n, kv, ctx, lo, MT;
+  __device__ __forceinline__ int vis(int i, int TB) const { return max(lo, ctx + min(n, (i + 1) * TB)); }
+  // cost of tiles 0..mt-1 of one head: vis + kSegCost each, in closed form
+  __device__ __forceinline__ long cost(int mt, int TB) const {
+    const long star = lo > ctx ? min(MT, (lo - ctx) / TB) : 0;   // the tiles with ctx + (i + 1) TB <= lo
+    long f = (long)mt * kSegCost + min((long)mt, star) * lo;
+    if (mt > star) {
+      f += (mt - star) * ctx + (long)TB * (((long)mt * (mt + 1) - star * (star + 1)) / 2);
+      if (mt == MT) f -= (long)ctx + (long)MT * TB - max(lo, ctx + n);
     }
+    return f;
   }
-  if (s < 0) return;
-  const int i = row - si.row0, ctx = si.kv - si.n;
-  for (int d = lane; d < D; d += kWave) qs[d] = bf16_to_f32(a.q[(size_t)row * a.q_stride + (size_t)h * D + d]);
-  const float ks = kFp8 ? a.k_scale[hk] : 1.f, vs = kFp8 ? a.v_scale[hk] : 1.f;
-  const uint64_t mask = a.tree_mask ? a.tree_mask[row] : 0;
-  const int pre = a.prefix_lens ? a.prefix_lens[s] : 0;
-  const int ps_mask = (1 << a.page_shift) - 1;
-  float m = -INFINITY, l = 0.f, o[D / kWave] = {};
+};
+__device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, int s, int TB) {
+  const SeqInfo q = seq_info(a, s);
+  SeqTiles t;
+  t.row0 = q.row0;
+  t.n = q.n;
+  t.kv = q.kv;
+  t.ctx = q.kv - q.n;
+  t.lo = a.tree_mask ? q.kv : (a.prefix_lens ? min(max(a.prefix_lens[s], 0), q.kv) : 0);
+  t.MT = (q.n + TB - 1) / TB;
+  return t;
+}
+
+// the same for a sequence that is one for the whole wave, held in scalar registers
+__device__ __forceinline__ SeqTiles uniform_seq(const AttnArgs& a, int s, int TB) {
+  SeqTiles t = seq_tiles(a, s, TB);
+  t.row0 = uni(t.row0); t.n = uni(t.n); t.kv = uni(t.kv); t.ctx = uni(t.ctx); t.lo = uni(t.lo); t.MT = uni(t.MT);
+  return t;
+}
+
+struct PartDesc {   // a segment that begins in part w and ends in a later part `last`
+  int row0, rows, head, last;
+};
+
+// Part w of `parts` covers [begin(w), begin(w + 1)) of `total` units.
+struct Parts {
+  long q, rem;
+  __device__ __forceinline__ Parts(long total, int parts) : q(total / parts), rem(total % parts) {}
+  __device__ __forceinline__ long begin(int w) const { return q * w + min((long)w, rem); }
+  __device__ __forceinline__ int of(long unit) const {   // the part that holds a unit
+    const long big = (q + 1) * rem;
+    return (int)(unit < big ? unit / (q + 1) : rem + (unit - big) / q);
+  }
+};
+
+// -------------------------------------------------------------------------------------- the kernel
+template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
+struct Attn {
+  static constexpr int kWaves = RW * KW;
+  static constexpr int M = 32 * QT * RW;
+  static constexpr int ES = FP8 ? 1 : 2;
+  static constexpr int RB = D * ES;             // bytes of a key's row
+  static constexpr int CPR = RB / 16;           // its 16-byte chunks
+  static constexpr int RPI = 64 / CPR;          // rows per 1 KB load
+  static constexpr int TILE = NK * RB;          // bytes of a K (or V) tile
+  static constexpr int NX = TILE / 1024;        // loads per tile
+  static constexpr int XW = NX / RW;            // of one wave
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int LDS = 2 * STAGE * KW;
+  static constexpr int KT = NK / 32;            // 32-key tiles of scores
+  static constexpr int DT = D / 32;
+  static constexpr int STEPS = D / 16;
+  static constexpr int SLOT = M * D + 2 * M;    // floats of a partial: O [M][D], then m and l per row
+  static_assert(NX % RW == 0 && RPI <= 16 && NK <= 64, "tile shape");
+  static_assert(KW == 1 || M * D * 4 <= 2 * STAGE, "the waves' sums are joined in their stages");
+};
+
+template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
+__global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs a, const int TB, const int parts_max,
+                                                                 float* __restrict__ partials,
+                                                                 PartDesc* __restrict__ descs) {
+  using C = Attn<D, FP8, QT, RW, KW, NK, CAP>;
+  constexpr int kThreads = 64 * C::kWaves;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
+  __shared__ long scan_sum[C::kWaves];
+  __shared__ long found_rem;
+  __shared__ int found_seq;
+  __shared__ float row_m[KW][C::M], row_l[KW][C::M];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  const int rw = wave % RW, kw = wave / RW;
+  const int half = lane >> 5, col = lane & 31;
+  // consecutive parts on one XCD: they walk neighbouring keys
+  const int w = (int)(blockIdx.x & 7) * (parts_max >> 3) + (int)(blockIdx.x >> 3);
+
+  // -------- which part of the line of segments is this workgroup's
+  const int per = (a.S + kThreads - 1) / kThreads;
+  const int s_lo = min(tid * per, a.S), s_hi = min(s_lo + per, a.S);
+  long mine = 0;
+  for (int s = s_lo; s < s_hi; ++s) {
+    const SeqTiles t = seq_tiles(a, s, TB);
+    mine += t.cost(t.MT, TB) * a.Hkv;
+  }
+  long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const long o = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) scan_sum[wave] = incl;
   __syncthreads();
-  for (int j0 = 0; j0 < si.kv; j0 += kWave) {
-    const int j = j0 + lane;
-    long e = -1;
-    bool see = j < si.kv;
-    if (see) {
-      const int page = a.block_table[(size_t)s * a.max_pages + (j >> a.page_shift)];
-      if (page >= 0 && page < a.num_pages)
-        e = (long)page * (long)a.page_stride + (long)((hk << a.page_shift) + (j & ps_mask)) * D;
-      const int b = j - ctx;
-      see = e >= 0 && (b < 0 || (a.tree_mask ? ((mask >> b) & 1) != 0 : b <= i) || j < pre);
-      if (a.tree_mask && b < 0) see = e >= 0;
-    }
-    float z = -INFINITY;
-    if (see) {
-      float dot = 0.f;
-      for (int d = 0; d < D; ++d) {
-        const float k = kFp8 ? e4m3_to_f32(static_cast<const uint8_t*>(a.k_cache)[e + d])
-                             : bf16_to_f32(static_cast<const uint16_t*>(a.k_cache)[e + d]);
-        dot += qs[d] * k;
-      }
-      z = dot * ks * a.scale;
-      if (a.softcap > 0.f) z = a.softcap * tanhf(z / a.softcap);
-    }
-    const float mn = fmaxf(m, wave_max(z));
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float p = expf(z - ref), f = expf(m - ref);
-    float sum = p;
-    for (int w = 1; w < kWave; w <<= 1) sum += __shfl_xor(sum, w, kWave);
-    l = l * f + sum;
-    m = mn;
-    ps[lane] = p;
-    base[lane] = see ? e : -1;
-    __syncthreads();
-    for (int c = 0; c < D / kWave; ++c) o[c] *= f;
-    for (int k = 0; k < kWave; ++k) {
-      const long b = base[k];
-      if (b < 0) continue;
-      for (int c = 0; c < D / kWave; ++c) {
-        const float v = kFp8 ? e4m3_to_f32(static_cast<const uint8_t*>(a.v_cache)[b + c * kWave + lane])
-                             : bf16_to_f32(static_cast<const uint16_t*>(a.v_cache)[b + c * kWave + lane]);
-        o[c] += ps[k] * v;
-      }
-    }
-    __syncthreads();
+  long total = 0, before = incl - mine;
+#pragma unroll
+  for (int i = 0; i < C::kWaves; ++i) {
+    if (i < wave) before += scan_sum[i];
+    total += scan_sum[i];
   }
-  for (int c = 0; c < D / kWave; ++c)
-    a.out[((size_t)row * a.Hq + h) * D + c * kWave + lane] = f32_to_bf16(l > 0.f ? o[c] * vs / l : 0.f);
-  if (a.lse && lane == 0) a.lse[(size_t)row * a.Hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  total = uni(total);
+  if (tid == 0) descs[w] = PartDesc{0, 0, 0, 0};
+  if (total == 0) return;
+  const int parts = (int)min((long)parts_max, (total + kMinPart - 1) / kMinPart);
+  if (w >= parts) return;
+  const Parts split(total, parts);
+  long u = split.begin(w);
+  const long u_end = split.begin(w + 1);
+  if (mine > 0 && u >= before && u < before + mine) {
+    long r = u - before;
+    for (int s = s_lo; s < s_hi; ++s) {
+      const SeqTiles t = seq_tiles(a, s, TB);
+      const long c = t.cost(t.MT, TB) * a.Hkv;
+      if (r < c) {
+        found_seq = s;
+        found_rem = r;
+        break;
+      }
+      r -= c;
+    }
+  }
+  __syncthreads();
+  int s = uni(found_seq);
+  long rem = uni(found_rem);
+  SeqTiles seq = uniform_seq(a, s, TB);
+  int h, mt;
+  {
+    const long per_head = seq.cost(seq.MT, TB);
+    h = uni((int)(rem / per_head));
+    rem -= h * per_head;
+    int lo = 0, hi = seq.MT;   // the largest tile with cost(tile) <= rem
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (seq.cost(mid, TB) <= rem) lo = mid;
+      else hi = mid;
+    }
+    mt = uni(lo);
+    rem -= seq.cost(mt, TB);
+  }
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)sm;
+  uint8_t* const stages = sm + kw * 2 * C::STAGE;
+  const uint32_t stages_off = lds0 + kw * 2 * C::STAGE;
+  const int page_mask = (1 << a.page_shift) - 1;
+  const size_t page_bytes = a.page_stride * C::ES;
+  const float scale2 = a.scale * kLog2e;
+  constexpr float kBias = FP8 ? 7.0f : 0.0f;   // float16 weights: 2^7 keeps small ones off its subnormals
+
+  // -------- this wave's LDS read addresses (see the layout above)
+  int k_addr, v_addr, v_addr2;
+  {
+    k_addr = col * C::RB + (((half ^ swizzle(col, C::CPR)) & (C::CPR - 1)) << 4);
+    const int dh = (lane >> 4) & 1, i = lane & 15;
+    if (FP8) {
+      const int r = i >> 1, key = 4 * half + (r & 3) + 8 * (r >> 2);
+      v_addr = key * C::RB + ((dh ^ swizzle(key, C::CPR)) << 4) + 8 * (i & 1);
+      v_addr2 = 0;
+    } else {
+      const int key = 4 * half + (i >> 2), c = 2 * dh + ((i & 3) >> 1);
+      v_addr = key * C::RB + ((c ^ swizzle(key, C::CPR)) << 4) + 8 * (i & 1);
+      v_addr2 = (key + 8) * C::RB + ((c ^ swizzle(key + 8, C::CPR)) << 4) + 8 * (i & 1);
+    }
+  }
+
+  while (u < u_end) {
+    // -------- the segment: rows, keys, and this part's share of its tiles
+    const int vis = seq.vis(mt, TB);
+    const long seg_cost = vis + kSegCost;
+    const long seg_end = u - rem + seg_cost;
+    const bool begins = rem == 0, ends = seg_end <= u_end;
+    const int ntiles = (vis + NK - 1) / NK;
+    const int t0 = min(ntiles, (int)(rem / NK));
+    const int t1 = ends ? ntiles : min(ntiles, (int)((rem + u_end - u) / NK));
+    const int tok0 = mt * TB, rows = min(TB, seq.n - tok0) * a.G;
+    const int row0 = seq.row0 + tok0;
+    const float ks = FP8 ? a.k_scale[h] : 1.f;
+    const float c = CAP ? 2.f * kLog2e * a.scale * ks / a.softcap : scale2 * ks;
+    const float cap2 = a.softcap * kLog2e;
+    const int* table = a.block_table + (size_t)s * a.max_pages;
+    const int pages_used = (seq.kv + page_mask) >> a.page_shift;
+    const uint8_t* const kc = static_cast<const uint8_t*>(a.k_cache) + ((size_t)h << a.page_shift) * C::RB;
+    const uint8_t* const vc = static_cast<const uint8_t*>(a.v_cache) + ((size_t)h << a.page_shift) * C::RB;
+
+    bf16x8 q[QT][C::STEPS];
+    int lim[QT];
+    uint64_t word[QT];
+#pragma unroll
+    for (int x = 0; x < QT; ++x) {
+      // rows past the tile's last repeat it and are not stored
+      const int r = min((rw * QT + x) * 32 + col, rows - 1);
+      const int tok = r / a.G, qrow = row0 + tok;
+      const uint16_t* p = a.q + (size_t)qrow * a.q_stride + (size_t)(h * a.G + r - tok * a.G) * D;
+#pragma unroll
+      for (int st = 0; st < C::STEPS; ++st) {
+        const int d = FP8 ? 32 * (st >> 1) + 16 * half + 8 * (st & 1) : 16 * st + 8 * half;
+        q[x][st] = *reinterpret_cast<const bf16x8*>(p + d);
+      }
+      if (a.tree_mask) {
+        lim[x] = max(seq.ctx, 0);
+        word[x] = a.tree_mask[qrow] & (~0ull >> (64 - seq.n));
+      } else {
+        lim[x] = max(seq.lo, seq.ctx + tok0 + tok + 1);
+        word[x] = 0;
+      }
+    }
+    // keys below this are seen by every row
+    const int all_see = a.tree_mask ? max(seq.ctx, 0) : max(seq.lo, seq.ctx + tok0 + 1);
+
+    v16f o[QT][C::DT];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int x = 0; x < QT; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+#pragma unroll
+      for (int d = 0; d < C::DT; ++d) o[x][d] = v16f{};
+    }
+
+    // -------- page ids: 64 at a time, one per lane; pages outside the pool (and past the last
+    // cached token) are read as page 0 and masked
+    int pg = 0, pg_base = -64;
+    bool careful = false;   // a page outside the pool was met
+    auto refill = [&](int first) {
+      pg_base = first;
+      const int i = first + lane;
+      const int id = i < pages_used ? table[i] : 0;
+      const bool bad = id < 0 || id >= a.num_pages;
+      careful = careful || __ballot(bad) != 0;
+      pg = bad ? 0 : id;
+    };
+    auto group_base = [&](const uint8_t* cache, int key) -> const uint8_t* {   // rows key .. key + 15
+      const int i = key >> a.page_shift;
+      const int id = __builtin_amdgcn_readlane(pg, i - pg_base);
+      return cache + (size_t)id * page_bytes + (size_t)(key & page_mask) * C::RB;
+    };
+    // a tile's keys lie in pages [key0 >> shift, (key0 + NK - 1) >> shift]: at most 4 of them
+    auto pages_for = [&](int key0) {
+      const int i = key0 >> a.page_shift;
+      if (i + (NK - 1) / 16 >= pg_base + 64 || i < pg_base) refill(i);
+    };
+    auto issue = [&](const uint8_t* cache, uint32_t lds, int key0) {
+#pragma unroll
+      for (int y = 0; y < C::XW; ++y) {
+        const int x = rw * C::XW + y;
+        const int row = x * C::RPI;
+        const uint8_t* base = group_base(cache, key0 + (row & ~15)) + (row & 15) * C::RB;
+        const int lr = lane / C::CPR;
+        const uint32_t voff = lr * C::RB + (((lane % C::CPR) ^ swizzle(row + lr, C::CPR)) << 4);
+        load_lds16(lds + x * 1024, voff, base);
+      }
+    };
+    // is the 16-key group that holds `key` in a page of the pool
+    auto group_ok = [&](int key) -> bool {
+      if (key >= seq.kv) return false;
+      const int id = table[key >> a.page_shift];
+      return id >= 0 && id < a.num_pages;
+    };
+    // V rows that no cached token stands behind may hold anything: zero, since 0 * NaN is NaN
+    auto zero_rows = [&](uint8_t* v, int key0) {
+#pragma unroll
+      for (int y = 0; y < C::XW; ++y) {
+        const int x = rw * C::XW + y;
+        const int key = key0 + x * C::RPI + lane / C::CPR;
+        if (key >= seq.kv || (careful && !group_ok(key)))
+          *reinterpret_cast<uint4*>(v + x * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
+      }
+    };
+
+    // -------- scores of one key tile
+    v16f sc[QT][C::KT];
+    auto scores = [&](const uint8_t* kt_lds) {
+#pragma unroll
+      for (int x = 0; x < QT; ++x)
+#pragma unroll
+        for (int t = 0; t < C::KT; ++t) sc[x][t] = v16f{};
+#pragma unroll
+      for (int t = 0; t < C::KT; ++t) {
+        if constexpr (FP8) {
+#pragma unroll
+          for (int s2 = 0; s2 < C::STEPS / 2; ++s2) {
+            const i32x4 raw = *reinterpret_cast<const i32x4*>(kt_lds + t * 32 * C::RB + (k_addr ^ (s2 * 32)));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              bf16x8 k;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * e + i], 1.0f, false);
+                const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * e + i], 1.0f, true);
+                k[4 * i] = lo[0]; k[4 * i + 1] = lo[1]; k[4 * i + 2] = hi[0]; k[4 * i + 3] = hi[1];
+              }
+#pragma unroll
+              for (int x = 0; x < QT; ++x)
+                sc[x][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][2 * s2 + e], sc[x][t], 0, 0, 0);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int st = 0; st < C::STEPS; ++st) {
+            const bf16x8 k = *reinterpret_cast<const bf16x8*>(kt_lds + t * 32 * C::RB + (k_addr ^ (st * 32)));
+#pragma unroll
+            for (int x = 0; x < QT; ++x)
+              sc[x][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][st], sc[x][t], 0, 0, 0);
+          }
+        }
+      }
+    };
+
+    // -------- masks, softmax step, weights as the next product's operand
+    bf16x8 pb[QT][NK / 16];
+    f16x8 pf[QT][NK / 16];
+    auto softmax = [&](int key0) {
+      const bool masked = key0 + NK > all_see || careful;
+#pragma unroll
+      for (int x = 0; x < QT; ++x) {
+        if constexpr (CAP) {
+#pragma unroll
+          for (int t = 0; t < C::KT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              // cap tanh(y) = cap (1 - 2 / (e^2y + 1)), in units of log2 e
+              const float e = __builtin_amdgcn_exp2f(sc[x][t][i] * c);
+              sc[x][t][i] = cap2 - 2.f * cap2 * __builtin_amdgcn_rcpf(e + 1.f);
+            }
+        }
+        if (masked) {
+          // bit k: key0 + k is seen
+          const int n = lim[x] - key0;
+          uint64_t see = n >= 64 ? ~0ull : (n <= 0 ? 0ull : ~0ull >> (64 - n));
+          if (a.tree_mask) {
+            const int b = key0 - seq.ctx;   // the first key's bit
+            see |= b >= 64 || b <= -64 ? 0ull : (b >= 0 ? word[x] >> b : word[x] << -b);
+          }
+          if (careful) {
+#pragma unroll
+            for (int g = 0; g < NK / 16; ++g)
+              if (!group_ok(key0 + 16 * g)) see &= ~(0xFFFFull << (16 * g));
+          }
+          see >>= 4 * half;
+#pragma unroll
+          for (int t = 0; t < C::KT; ++t) {
+            const uint32_t bits = (uint32_t)(see >> (32 * t));
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              sc[x][t][i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? sc[x][t][i] : -INFINITY;
+          }
+        }
+        float mx = sc[x][0][0];
+#pragma unroll
+        for (int t = 0; t < C::KT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[x][t][i]);
+        mx = swap_max(mx);
+        mx = (CAP ? mx : mx * c) - kBias;
+        if (__any(mx > m[x] + kMoveMax)) {
+          const float mn = fmaxf(m[x], mx);
+          const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - mn);
+          m[x] = mn;
+          l[x] *= f;
+#pragma unroll
+          for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[x][d][i] *= f;
+        }
+        const float ms = m[x] == -INFINITY ? 0.f : m[x];
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < C::KT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float z = CAP ? sc[x][t][i] - ms : __builtin_fmaf(sc[x][t][i], c, -ms);
+            const float p = __builtin_amdgcn_exp2f(z);
+            sum += p;
+            if constexpr (FP8) pf[x][2 * t + i / 8][i % 8] = (_Float16)p;
+            else pb[x][2 * t + i / 8][i % 8] = (__bf16)p;
+          }
+        l[x] += sum;
+      }
+    };
+
+    auto values = [&](const uint8_t* v) {
+#pragma unroll
+      for (int st = 0; st < NK / 16; ++st)
+#pragma unroll
+        for (int d = 0; d < C::DT; ++d) {
+          if constexpr (FP8) {
+            const i32x2 raw = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (__attribute__((address_space(3))) i32x2*)(v + st * 16 * C::RB + (v_addr ^ (32 * d))));
+            f16x8 f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw[i], 1.0f, false);
+              const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw[i], 1.0f, true);
+              f[4 * i] = lo[0]; f[4 * i + 1] = lo[1]; f[4 * i + 2] = hi[0]; f[4 * i + 3] = hi[1];
+            }
+#pragma unroll
+            for (int x = 0; x < QT; ++x)
+              o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, pf[x][st], o[x][d], 0, 0, 0);
+          } else {
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(v + st * 16 * C::RB + (v_addr ^ (64 * d))));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(v + st * 16 * C::RB + (v_addr2 ^ (64 * d))));
+            const bf16x8 f = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int x = 0; x < QT; ++x)
+              o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[x][st], o[x][d], 0, 0, 0);
+          }
+        }
+    };
+
+    // -------- the key loop
+    if constexpr (RW == 1) {
+      // this wave's own tiles; two stages in flight. Loads are issued in the order K0 V0 K1 V1 | K2
+      // (after the scores of tile 0) V2 (after its values) ..., so with L = NX loads per tile the
+      // ones younger than K_t are V_t K_t+1 V_t+1, and those younger than V_t K_t+1 V_t+1 K_t+2
+      constexpr int L = C::NX;
+      const int cnt = t1 - t0;
+      const int wt0 = t0 + (int)((long)cnt * kw / KW), wt1 = t0 + (int)((long)cnt * (kw + 1) / KW);
+      for (int t = wt0; t < min(wt0 + 2, wt1); ++t) {
+        const uint32_t st = stages_off + ((t - wt0) & 1) * C::STAGE;
+        pages_for(t * NK);
+        issue(kc, st, t * NK);
+        issue(vc, st + C::TILE, t * NK);
+      }
+      for (int t = wt0; t < wt1; ++t) {
+        const int b = (t - wt0) & 1, left = wt1 - 1 - t;
+        uint8_t* const st = stages + b * C::STAGE;
+        const uint32_t st_off = stages_off + b * C::STAGE;
+        if (left == 0) wait_vm<L>();
+        else wait_vm<3 * L>();
+        scores(st);
+        if (left >= 2) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // K_t has been read
+          pages_for((t + 2) * NK);
+          issue(kc, st_off, (t + 2) * NK);
+        }
+        softmax(t * NK);
+        if (left == 0) wait_vm<0>();
+        else if (left == 1) wait_vm<2 * L>();
+        else wait_vm<3 * L>();
+        if ((t + 1) * NK > seq.kv || careful) {
+          zero_rows(st + C::TILE, t * NK);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        values(st + C::TILE);
+        if (left >= 2) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // V_t has been read
+          issue(vc, st_off + C::TILE, (t + 2) * NK);
+        }
+      }
+    } else {
+      // the waves share a tile: loaded one tile ahead into the other stage, one barrier per tile
+      if (t0 < t1) {
+        pages_for(t0 * NK);
+        issue(kc, stages_off, t0 * NK);
+        issue(vc, stages_off + C::TILE, t0 * NK);
+      }
+      for (int t = t0; t < t1; ++t) {
+        const int b = (t - t0) & 1;
+        uint8_t* const st = stages + b * C::STAGE;
+        wait_vm<0>();
+        if ((t + 1) * NK > seq.kv || careful) zero_rows(st + C::TILE, t * NK);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (t + 1 < t1) {
+          const uint32_t nx = stages_off + (b ^ 1) * C::STAGE;
+          pages_for((t + 1) * NK);
+          issue(kc, nx, (t + 1) * NK);
+          issue(vc, nx + C::TILE, (t + 1) * NK);
+        }
+        scores(st);
+        softmax(t * NK);
+        values(st + C::TILE);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // before the stages are filled again
+    }
+
+    // -------- the segment's result, or this part's partial
+    const bool whole = begins && ends;
+    float* const slot = partials + (size_t)(2 * w + (begins ? 1 : 0)) * C::SLOT;
+    const float vs = FP8 ? a.v_scale[h] : 1.f;
+    if constexpr (KW == 1) {
+#pragma unroll
+      for (int x = 0; x < QT; ++x) {
+        const int r = (rw * QT + x) * 32 + col;
+        const float sum = swap_sum(l[x]);
+        if (r < rows) {
+          if (whole) {
+            const int tok = r / a.G, head = h * a.G + r - tok * a.G;
+            const size_t at = (size_t)(row0 + tok) * a.Hq + head;
+            const float f = sum > 0.f ? vs / sum : 0.f;
+#pragma unroll
+            for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint2*>(a.out + at * D + 32 * d + 8 * i + 4 * half) =
+                    make_uint2(pack_bf16x2(o[x][d][4 * i] * f, o[x][d][4 * i + 1] * f),
+                               pack_bf16x2(o[x][d][4 * i + 2] * f, o[x][d][4 * i + 3] * f));
+            if (a.lse && half == 0) a.lse[at] = sum > 0.f ? (m[x] + log2f(sum)) * kLn2 : -INFINITY;
+          } else {
+#pragma unroll
+            for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(slot + (size_t)r * D + 32 * d + 8 * i + 4 * half) =
+                    make_float4(o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]);
+            if (half == 0) {
+              slot[C::M * D + r] = m[x];
+              slot[C::M * D + C::M + r] = sum;
+            }
+          }
+        }
+      }
+    } else {
+      // every wave's O, [row][D] float32 with chunks swapped by row, in its own stages
+#pragma unroll
+      for (int x = 0; x < QT; ++x) {
+        const int r = x * 32 + col;
+        const float sum = swap_sum(l[x]);
+        if (half == 0) {
+          row_m[kw][r] = m[x];
+          row_l[kw][r] = sum;
+        }
+#pragma unroll
+        for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int chunk = (8 * d + 2 * i + half) ^ (r & 15);
+            *reinterpret_cast<float4*>(stages + r * D * 4 + chunk * 16) =
+                make_float4(o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]);
+          }
+      }
+      __syncthreads();
+      for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c4 = i % (D / 4);
+        float mx = row_m[0][r];
+#pragma unroll
+        for (int k = 1; k < KW; ++k) mx = fmaxf(mx, row_m[k][r]);
+        float sum = 0.f, v0 = 0.f, v1 = 0.f, v2 = 0.f, v3 = 0.f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+          const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(row_m[k][r] - mx);
+          const float4 v = *reinterpret_cast<const float4*>(sm + k * 2 * C::STAGE + r * D * 4 + ((c4 ^ (r & 15)) * 16));
+          sum += f * row_l[k][r];
+          v0 += f * v.x; v1 += f * v.y; v2 += f * v.z; v3 += f * v.w;
+        }
+        if (whole) {
+          const int tok = r / a.G, head = h * a.G + r - tok * a.G;
+          const size_t at = (size_t)(row0 + tok) * a.Hq + head;
+          const float f = sum > 0.f ? vs / sum : 0.f;
+          *reinterpret_cast<uint2*>(a.out + at * D + 4 * c4) =
+              make_uint2(pack_bf16x2(v0 * f, v1 * f), pack_bf16x2(v2 * f, v3 * f));
+          if (a.lse && c4 == 0) a.lse[at] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        } else {
+          *reinterpret_cast<float4*>(slot + (size_t)r * D + 4 * c4) = make_float4(v0, v1, v2, v3);
+          if (c4 == 0) {
+            slot[C::M * D + r] = mx;
+            slot[C::M * D + C::M + r] = sum;
+          }
+        }
+      }
+      __syncthreads();   // the stages are free again
+    }
+    if (begins && !ends && tid == 0) descs[w] = PartDesc{row0, rows, h, split.of(seg_end - 1)};
+
+    // -------- the next segment
+    u = min(u_end, seg_end);
+    rem = 0;
+    if (++mt >= seq.MT) {
+      mt = 0;
+      if (++h >= a.Hkv && u < u_end) {
+        h = 0;
+        do seq = uniform_seq(a, ++s, TB);
+        while (seq.n == 0);
+      }
+    }
+  }
 }
 
-size_t attention_workspace_bytes(int, int, int, int, int) { return 0; }
-
-template <bool kFp8>
-static void launch_plain(const AttnArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.T, (unsigned)a.Hq);
-  switch (a.D) {
-    case 64: hipLaunchKernelGGL((attention_plain_kernel<64, kFp8>), grid, dim3(64), 0, stream, a); break;
-    case 128: hipLaunchKernelGGL((attention_plain_kernel<128, kFp8>), grid, dim3(64), 0, stream, a); break;
-    default: hipLaunchKernelGGL((attention_plain_kernel<256, kFp8>), grid, dim3(64), 0, stream, a); break;
+// Joins the partials of segments that span several parts: workgroup (w, y) takes rows y, y +
+// gridDim.y, ... of the segment that begins in part w. A wave reads D floats of several partials
+// per load; 4 waves and 8 loads in flight hide the latency of a segment split over the whole card.
+template <int D>
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, const int M,
+                                                             const float* __restrict__ partials,
+                                                             const PartDesc* __restrict__ descs) {
+  constexpr int LPR = D / 4;              // lanes per partial row (16 bytes each)
+  constexpr int PPB = 256 / LPR;          // partials side by side in the workgroup
+  __shared__ float4 acc[256];
+  __shared__ float acc_l[PPB], acc_m[PPB];
+  const int w = blockIdx.x;
+  const PartDesc d = descs[w];
+  const size_t slot = (size_t)M * D + 2 * M;
+  const int c4 = threadIdx.x % LPR, p0 = threadIdx.x / LPR;
+  const float vs = a.v_scale && d.rows > 0 ? a.v_scale[d.head] : 1.f;
+  for (int r = blockIdx.y; r < d.rows; r += gridDim.y) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = w + p0; p <= d.last; p += PPB) {
+      const float* s = partials + (size_t)(p == w ? 2 * w + 1 : 2 * p) * slot;
+      const float pm = s[(size_t)M * D + r], pl = s[(size_t)M * D + M + r];
+      const float4 v = *reinterpret_cast<const float4*>(s + (size_t)r * D + 4 * c4);
+      const float mn = fmaxf(m, pm);
+      if (pl > 0.f) {   // an empty partial says nothing
+        const float f = __builtin_amdgcn_exp2f(m - mn), g = __builtin_amdgcn_exp2f(pm - mn);
+        m = mn;
+        l = l * f + pl * g;
+        o.x = o.x * f + v.x * g;
+        o.y = o.y * f + v.y * g;
+        o.z = o.z * f + v.z * g;
+        o.w = o.w * f + v.w * g;
+      }
+    }
+    acc[threadIdx.x] = o;
+    if (c4 == 0) {
+      acc_m[p0] = m;
+      acc_l[p0] = l;
+    }
+    __syncthreads();
+    if (p0 == 0) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PPB; ++i) mx = fmaxf(mx, acc_m[i]);
+      float sum = 0.f, v0 = 0.f, v1 = 0.f, v2 = 0.f, v3 = 0.f;
+#pragma unroll
+      for (int i = 0; i < PPB; ++i) {
+        const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(acc_m[i] - mx);
+        const float4 v = acc[i * LPR + c4];
+        sum += f * acc_l[i];
+        v0 += f * v.x; v1 += f * v.y; v2 += f * v.z; v3 += f * v.w;
+      }
+      const int tok = r / a.G;
+      const size_t at = (size_t)(d.row0 + tok) * a.Hq + d.head * a.G + r - tok * a.G;
+      const float f = sum > 0.f ? vs / sum : 0.f;
+      *reinterpret_cast<uint2*>(a.out + at * D + 4 * c4) =
+          make_uint2(pack_bf16x2(v0 * f, v1 * f), pack_bf16x2(v2 * f, v3 * f));
+      if (a.lse && c4 == 0) a.lse[at] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    }
+    __syncthreads();
   }
+}
+
+// ------------------------------------------------------------------------------------- the launch
+constexpr int kParts = 256;   // one workgroup per CU
+
+// Rows of a workgroup's tile for calls of at most max_q tokens per sequence
+static int tile_rows(int max_q, int G, int D) {
+  const long rows = (long)max_q * G;
+  return rows <= 32 ? 32 : (rows <= 64 && D < 256 ? 64 : 128);
+}
+static size_t slot_floats(int M, int D) { return (size_t)M * D + 2 * M; }
+
+size_t attention_workspace_bytes(int S, int max_q, int Hq, int Hkv, int D) {
+  (void)S;
+  return 2 * kParts * slot_floats(tile_rows(max_q, Hq / Hkv, D), D) * 4 + kParts * sizeof(PartDesc);
+}
+
+template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
+static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
+  using C = Attn<D, FP8, QT, RW, KW, NK, CAP>;
+  auto* kernel = attention_kernel<D, FP8, QT, RW, KW, NK, CAP>;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+  if (e != hipSuccess) return e;
+  float* partials = static_cast<float*>(a.ws);
+  PartDesc* descs = reinterpret_cast<PartDesc*>(partials + 2 * kParts * slot_floats(C::M, D));
+  hipLaunchKernelGGL(kernel, dim3(kParts), dim3(64 * C::kWaves), C::LDS, stream, a, C::M / a.G, kParts, partials,
+                     descs);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(attention_join_kernel<D>, dim3(kParts, C::M / 4), dim3(256), 0, stream, a, C::M,
+                     (const float*)partials, (const PartDesc*)descs);
+  return hipGetLastError();
+}
+
+template <int D, bool FP8, bool CAP>
+static hipError_t launch_rows(const AttnArgs& a, hipStream_t stream) {
+  constexpr int NKs = FP8 || D == 64 ? (D == 256 ? 32 : 64) : 32;
+  const int M = tile_rows(a.max_q, a.G, D);
+  if (M == 32) return launch_one<D, FP8, 1, 1, D == 256 ? 2 : 4, NKs, CAP>(a, stream);
+  if constexpr (D < 256) {
+    if (M == 64) return launch_one<D, FP8, 2, 1, 4, D == 64 && FP8 ? 64 : NKs, CAP>(a, stream);
+  }
+  return launch_one<D, FP8, 1, 4, 1, D == 256 ? 32 : 64, CAP>(a, stream);
+}
+
+template <int D>
+static hipError_t launch_dim(const AttnArgs& a, hipStream_t stream) {
+  const bool cap = a.softcap > 0.f;
+  if (a.k_scale) return cap ? launch_rows<D, true, true>(a, stream) : launch_rows<D, true, false>(a, stream);
+  return cap ? launch_rows<D, false, true>(a, stream) : launch_rows<D, false, false>(a, stream);
 }
 
 hipError_t launch_attention(const AttnArgs& a, hipStream_t stream) {
-  if (a.k_scale)
-    launch_plain<true>(a, stream);
-  else
-    launch_plain<false>(a, stream);
-  return hipGetLastError();
+  switch (a.D) {
+    case 64: return launch_dim<64>(a, stream);
+    case 128: return launch_dim<128>(a, stream);
+    default: return launch_dim<256>(a, stream);
+  }
 }
 
 }  // namespace srmoe
