@@ -50,10 +50,13 @@ constexpr float kMoveMax = 8.0f;    // a running maximum moves when a score exce
 constexpr int kSegCost = 64;        // a segment's fixed cost, in keys, for the work split
 constexpr int kMinPart = 256;       // a part holds at least this many keys' cost
 
-// 16-byte chunk swap of key k's row (CPR chunks): distinct for 8 consecutive keys (reads of K) and
-// for {4h..4h+3, 8+4h..8+4h+3} of 16 keys (transposing reads of V).
+// 16-byte chunk swap of key k's row (CPR chunks of it), for LDS's 64 banks of 4 bytes: 16 consecutive
+// keys' same chunk (a step of K's reads) and the 64 or 32 bytes of {4h..4h+3} (8-bit: and 8+4h..) of a
+// transposing read of V fall on different banks (rows of 128 and 64 bytes: 2 and 4 rows span the
+// banks, so the low key bits need no swap).
 __device__ __forceinline__ int swizzle(int k, int cpr) {
-  return (((k & 3) << 1) | (((k >> 2) ^ (k >> 3)) & 1)) & (cpr - 1);
+  const int low = (k >> 2) & 3;
+  return cpr >= 16 ? ((k & 3) << 2) | low : (cpr == 8 ? ((k & 2) << 1) | low : low);
 }
 
 template <int N>
@@ -76,10 +79,36 @@ __device__ __forceinline__ long uni(long v) {
 
 // 16 bytes per lane from base + voff to LDS address `lds` + 16 * lane. In asm, because the
 // compiler would wait for every such load in flight before any later LDS read; wait_vm counts them.
+// kOnce: the bytes are read by this wave alone and passed through the caches as such (decode of 24
+// sequences of up to 16384 tokens, 0.93 GB: 170 us without, 152 us with).
+template <bool kOnce>
 __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t voff, const uint8_t* base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uni((int)lds)), "v"(voff),
-               "s"(uni((long)base))
-               : "memory");
+  if (kOnce)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(uni((int)lds)), "v"(voff),
+                 "s"(uni((long)base))
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uni((int)lds)), "v"(voff),
+                 "s"(uni((long)base))
+                 : "memory");
+}
+
+// LDS reads and matrix instructions stay on their side of this; other arithmetic may cross.
+__device__ __forceinline__ void fence_reads() { __builtin_amdgcn_sched_barrier(0x0006 | 0x0400); }
+// 8 e4m3 codes -> bf16 / float16 (both exact)
+__device__ __forceinline__ bf16x8 bf16_of_e4m3(int a, int b) {
+  const bf16x2_t p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+  const bf16x2_t q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+  const bf16x2_t r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+  const bf16x2_t s = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+  return bf16x8{p[0], p[1], q[0], q[1], r[0], r[1], s[0], s[1]};
+}
+__device__ __forceinline__ f16x8 f16_of_e4m3(int a, int b) {
+  const f16x2 p = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
+  const f16x2 q = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+  const f16x2 r = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
+  const f16x2 s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+  return f16x8{p[0], p[1], q[0], q[1], r[0], r[1], s[0], s[1]};
 }
 
 // ------------------------------------------------------------------------------- the work split
@@ -156,7 +185,8 @@ struct Attn {
 };
 
 template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
-__global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs a, const int TB, const int parts_max,
+__global__ void __launch_bounds__(64 * RW * KW)
+__attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 256 ? 2 : 1))) attention_kernel(const AttnArgs a, const int TB, const int parts_max,
                                                                  float* __restrict__ partials,
                                                                  PartDesc* __restrict__ descs) {
   using C = Attn<D, FP8, QT, RW, KW, NK, CAP>;
@@ -245,7 +275,7 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
   // -------- this wave's LDS read addresses (see the layout above)
   int k_addr, v_addr, v_addr2;
   {
-    k_addr = col * C::RB + (((half ^ swizzle(col, C::CPR)) & (C::CPR - 1)) << 4);
+    k_addr = col * C::RB + ((half ^ swizzle(col, C::CPR)) << 4);
     const int dh = (lane >> 4) & 1, i = lane & 15;
     if (FP8) {
       const int r = i >> 1, key = 4 * half + (r & 3) + 8 * (r >> 2);
@@ -299,6 +329,11 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
         word[x] = 0;
       }
     }
+    // q is here before the key loop: a wait for it inside would wait for the tiles in flight too
+#pragma unroll
+    for (int x = 0; x < QT; ++x)
+#pragma unroll
+      for (int st = 0; st < C::STEPS; ++st) asm volatile("" ::"v"(__builtin_bit_cast(i32x4, q[x][st])));
     // keys below this are seen by every row
     const int all_see = a.tree_mask ? max(seq.ctx, 0) : max(seq.lo, seq.ctx + tok0 + 1);
 
@@ -324,10 +359,9 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
       careful = careful || __ballot(bad) != 0;
       pg = bad ? 0 : id;
     };
-    auto group_base = [&](const uint8_t* cache, int key) -> const uint8_t* {   // rows key .. key + 15
-      const int i = key >> a.page_shift;
-      const int id = __builtin_amdgcn_readlane(pg, i - pg_base);
-      return cache + (size_t)id * page_bytes + (size_t)(key & page_mask) * C::RB;
+    auto group_offset = [&](int key) -> size_t {   // of rows key .. key + 15 in kc and vc
+      const int id = __builtin_amdgcn_readlane(pg, (key >> a.page_shift) - pg_base);
+      return (size_t)id * page_bytes + (size_t)(key & page_mask) * C::RB;
     };
     // a tile's keys lie in pages [key0 >> shift, (key0 + NK - 1) >> shift]: at most 4 of them
     auto pages_for = [&](int key0) {
@@ -339,10 +373,10 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
       for (int y = 0; y < C::XW; ++y) {
         const int x = rw * C::XW + y;
         const int row = x * C::RPI;
-        const uint8_t* base = group_base(cache, key0 + (row & ~15)) + (row & 15) * C::RB;
+        const uint8_t* base = cache + group_offset(key0 + (row & ~15)) + (row & 15) * C::RB;
         const int lr = lane / C::CPR;
         const uint32_t voff = lr * C::RB + (((lane % C::CPR) ^ swizzle(row + lr, C::CPR)) << 4);
-        load_lds16(lds + x * 1024, voff, base);
+        load_lds16<RW == 1>(lds + x * 1024, voff, base);
       }
     };
     // is the 16-key group that holds `key` in a page of the pool
@@ -362,53 +396,56 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
       }
     };
 
-    // -------- scores of one key tile
+    // -------- scores of one key tile. Each product's operand is read from LDS kAhead products
+    // earlier, and the fences keep that order: left alone, the compiler reads right before use and every
+    // product waits for its own read.
     v16f sc[QT][C::KT];
     auto scores = [&](const uint8_t* kt_lds) {
 #pragma unroll
       for (int x = 0; x < QT; ++x)
 #pragma unroll
         for (int t = 0; t < C::KT; ++t) sc[x][t] = v16f{};
+      constexpr int kReads = C::KT * C::STEPS / (FP8 ? 2 : 1);   // 16 bytes: one step of bf16, two of e4m3
+      constexpr int kAhead = FP8 ? 3 : 6;
+      i32x4 raw[kReads];
+      auto read = [&](int i) {
+        const int t = i % C::KT, st = i / C::KT;
+        raw[i] = *reinterpret_cast<const i32x4*>(kt_lds + t * 32 * C::RB + (k_addr ^ (st * 32)));
+      };
 #pragma unroll
-      for (int t = 0; t < C::KT; ++t) {
+      for (int i = 0; i < kAhead; ++i) read(i);
+      fence_reads();
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) {
+        if (i + kAhead < kReads) read(i + kAhead);
+        fence_reads();
+        const int t = i % C::KT, st = i / C::KT;
         if constexpr (FP8) {
 #pragma unroll
-          for (int s2 = 0; s2 < C::STEPS / 2; ++s2) {
-            const i32x4 raw = *reinterpret_cast<const i32x4*>(kt_lds + t * 32 * C::RB + (k_addr ^ (s2 * 32)));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              bf16x8 k;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * e + i], 1.0f, false);
-                const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * e + i], 1.0f, true);
-                k[4 * i] = lo[0]; k[4 * i + 1] = lo[1]; k[4 * i + 2] = hi[0]; k[4 * i + 3] = hi[1];
-              }
-#pragma unroll
-              for (int x = 0; x < QT; ++x)
-                sc[x][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][2 * s2 + e], sc[x][t], 0, 0, 0);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int st = 0; st < C::STEPS; ++st) {
-            const bf16x8 k = *reinterpret_cast<const bf16x8*>(kt_lds + t * 32 * C::RB + (k_addr ^ (st * 32)));
+          for (int e = 0; e < 2; ++e) {
+            const bf16x8 k = bf16_of_e4m3(raw[i][2 * e], raw[i][2 * e + 1]);
 #pragma unroll
             for (int x = 0; x < QT; ++x)
-              sc[x][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][st], sc[x][t], 0, 0, 0);
+              sc[x][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][2 * st + e], sc[x][t], 0, 0, 0);
           }
+        } else {
+          const bf16x8 k = __builtin_bit_cast(bf16x8, raw[i]);
+#pragma unroll
+          for (int x = 0; x < QT; ++x)
+            sc[x][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][st], sc[x][t], 0, 0, 0);
         }
+        fence_reads();
       }
     };
 
-    // -------- masks, softmax step, weights as the next product's operand
+    // -------- the softmax step in four pieces: caps and masks, the rows' maxima, a moved maximum, and
+    // the weights as the next product's operand
     bf16x8 pb[QT][NK / 16];
     f16x8 pf[QT][NK / 16];
-    auto softmax = [&](int key0) {
-      const bool masked = key0 + NK > all_see || careful;
+    auto mask = [&](int key0) {
+      if constexpr (CAP) {
 #pragma unroll
-      for (int x = 0; x < QT; ++x) {
-        if constexpr (CAP) {
+        for (int x = 0; x < QT; ++x)
 #pragma unroll
           for (int t = 0; t < C::KT; ++t)
 #pragma unroll
@@ -417,38 +454,50 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
               const float e = __builtin_amdgcn_exp2f(sc[x][t][i] * c);
               sc[x][t][i] = cap2 - 2.f * cap2 * __builtin_amdgcn_rcpf(e + 1.f);
             }
+      }
+      if (key0 + NK <= all_see && !careful) return;
+#pragma unroll
+      for (int x = 0; x < QT; ++x) {
+        // bit k: key0 + k is seen
+        const int n = lim[x] - key0;
+        uint64_t see = n >= 64 ? ~0ull : (n <= 0 ? 0ull : ~0ull >> (64 - n));
+        if (a.tree_mask) {
+          const int b = key0 - seq.ctx;   // the first key's bit
+          see |= b >= 64 || b <= -64 ? 0ull : (b >= 0 ? word[x] >> b : word[x] << -b);
         }
-        if (masked) {
-          // bit k: key0 + k is seen
-          const int n = lim[x] - key0;
-          uint64_t see = n >= 64 ? ~0ull : (n <= 0 ? 0ull : ~0ull >> (64 - n));
-          if (a.tree_mask) {
-            const int b = key0 - seq.ctx;   // the first key's bit
-            see |= b >= 64 || b <= -64 ? 0ull : (b >= 0 ? word[x] >> b : word[x] << -b);
-          }
-          if (careful) {
+        if (careful) {
 #pragma unroll
-            for (int g = 0; g < NK / 16; ++g)
-              if (!group_ok(key0 + 16 * g)) see &= ~(0xFFFFull << (16 * g));
-          }
-          see >>= 4 * half;
-#pragma unroll
-          for (int t = 0; t < C::KT; ++t) {
-            const uint32_t bits = (uint32_t)(see >> (32 * t));
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              sc[x][t][i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? sc[x][t][i] : -INFINITY;
-          }
+          for (int g = 0; g < NK / 16; ++g)
+            if (!group_ok(key0 + 16 * g)) see &= ~(0xFFFFull << (16 * g));
         }
-        float mx = sc[x][0][0];
+        see >>= 4 * half;
+#pragma unroll
+        for (int t = 0; t < C::KT; ++t) {
+          const uint32_t bits = (uint32_t)(see >> (32 * t));
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            sc[x][t][i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? sc[x][t][i] : -INFINITY;
+        }
+      }
+    };
+    float mx[QT];
+    auto maxima = [&]() {
+#pragma unroll
+      for (int x = 0; x < QT; ++x) {
+        float v = sc[x][0][0];
 #pragma unroll
         for (int t = 0; t < C::KT; ++t)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[x][t][i]);
-        mx = swap_max(mx);
-        mx = (CAP ? mx : mx * c) - kBias;
-        if (__any(mx > m[x] + kMoveMax)) {
-          const float mn = fmaxf(m[x], mx);
+          for (int i = 0; i < 16; ++i) v = fmaxf(v, sc[x][t][i]);
+        v = swap_max(v);
+        mx[x] = (CAP ? v : v * c) - kBias;
+      }
+    };
+    auto move_max = [&]() {
+#pragma unroll
+      for (int x = 0; x < QT; ++x)
+        if (__any(mx[x] > m[x] + kMoveMax)) {
+          const float mn = fmaxf(m[x], mx[x]);
           const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - mn);
           m[x] = mn;
           l[x] *= f;
@@ -457,14 +506,17 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[x][d][i] *= f;
         }
+    };
+    auto weights = [&](const v16f (&z)[QT][C::KT]) {
+#pragma unroll
+      for (int x = 0; x < QT; ++x) {
         const float ms = m[x] == -INFINITY ? 0.f : m[x];
         float sum = 0.f;
 #pragma unroll
         for (int t = 0; t < C::KT; ++t)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float z = CAP ? sc[x][t][i] - ms : __builtin_fmaf(sc[x][t][i], c, -ms);
-            const float p = __builtin_amdgcn_exp2f(z);
+            const float p = __builtin_amdgcn_exp2f(CAP ? z[x][t][i] - ms : __builtin_fmaf(z[x][t][i], c, -ms));
             sum += p;
             if constexpr (FP8) pf[x][2 * t + i / 8][i % 8] = (_Float16)p;
             else pb[x][2 * t + i / 8][i % 8] = (__bf16)p;
@@ -474,34 +526,43 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
     };
 
     auto values = [&](const uint8_t* v) {
-#pragma unroll
-      for (int st = 0; st < NK / 16; ++st)
-#pragma unroll
-        for (int d = 0; d < C::DT; ++d) {
-          if constexpr (FP8) {
-            const i32x2 raw = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                (__attribute__((address_space(3))) i32x2*)(v + st * 16 * C::RB + (v_addr ^ (32 * d))));
-            f16x8 f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw[i], 1.0f, false);
-              const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw[i], 1.0f, true);
-              f[4 * i] = lo[0]; f[4 * i + 1] = lo[1]; f[4 * i + 2] = hi[0]; f[4 * i + 3] = hi[1];
-            }
-#pragma unroll
-            for (int x = 0; x < QT; ++x)
-              o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, pf[x][st], o[x][d], 0, 0, 0);
-          } else {
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(v + st * 16 * C::RB + (v_addr ^ (64 * d))));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(v + st * 16 * C::RB + (v_addr2 ^ (64 * d))));
-            const bf16x8 f = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-            for (int x = 0; x < QT; ++x)
-              o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[x][st], o[x][d], 0, 0, 0);
-          }
+      constexpr int kReads = NK / 16 * C::DT;
+      constexpr int kAhead = 4;
+      i32x4 raw[kReads];
+      auto read = [&](int i) {
+        const int st = i / C::DT, d = i % C::DT;
+        if constexpr (FP8) {
+          const i32x2 r = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (__attribute__((address_space(3))) i32x2*)(v + st * 16 * C::RB + (v_addr ^ (32 * d))));
+          raw[i][0] = r[0];
+          raw[i][1] = r[1];
+        } else {
+          const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(v + st * 16 * C::RB + (v_addr ^ (64 * d)))));
+          const i32x2 hi = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(v + st * 16 * C::RB + (v_addr2 ^ (64 * d)))));
+          raw[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3);
         }
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) read(i);
+      fence_reads();
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) {
+        if (i + kAhead < kReads) read(i + kAhead);
+        fence_reads();
+        const int st = i / C::DT, d = i % C::DT;
+#pragma unroll
+        for (int x = 0; x < QT; ++x) {
+          if constexpr (FP8)
+            o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f16_of_e4m3(raw[i][0], raw[i][1]), pf[x][st], o[x][d],
+                                                             0, 0, 0);
+          else
+            o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, raw[i]), pb[x][st],
+                                                              o[x][d], 0, 0, 0);
+        }
+        fence_reads();
+      }
     };
 
     // -------- the key loop
@@ -530,7 +591,10 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
           pages_for((t + 2) * NK);
           issue(kc, st_off, (t + 2) * NK);
         }
-        softmax(t * NK);
+        mask(t * NK);
+        maxima();
+        move_max();
+        weights(sc);
         if (left == 0) wait_vm<0>();
         else if (left == 1) wait_vm<2 * L>();
         else wait_vm<3 * L>();
@@ -564,7 +628,10 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
           issue(vc, nx + C::TILE, (t + 1) * NK);
         }
         scores(st);
-        softmax(t * NK);
+        mask(t * NK);
+        maxima();
+        move_max();
+        weights(sc);
         values(st + C::TILE);
       }
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // before the stages are filled again
@@ -672,71 +739,95 @@ __global__ void __launch_bounds__(64 * RW * KW) attention_kernel(const AttnArgs 
   }
 }
 
-// Joins the partials of segments that span several parts: workgroup (w, y) takes rows y, y +
-// gridDim.y, ... of the segment that begins in part w. A wave reads D floats of several partials
-// per load; 4 waves and 8 loads in flight hide the latency of a segment split over the whole card.
+// Joins the partials of segments that span several parts: workgroup (w, y) takes rows of the
+// segment that begins in part w. D / 4 lanes read a partial's row (16 bytes each); the workgroup's
+// groups of such lanes stand side by side on `side` partials of a row (few partials: on rows of
+// their own), and each has 4 partials in flight, so that neither a segment split over the whole card
+// nor 128 rows of two partials each wait for memory more than a few times.
+constexpr int kJoinThreads = 512, kJoinY = 8;
 template <int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, const int M,
-                                                             const float* __restrict__ partials,
-                                                             const PartDesc* __restrict__ descs) {
-  constexpr int LPR = D / 4;              // lanes per partial row (16 bytes each)
-  constexpr int PPB = 256 / LPR;          // partials side by side in the workgroup
-  __shared__ float4 acc[256];
-  __shared__ float acc_l[PPB], acc_m[PPB];
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, const int M,
+                                                                      const float* __restrict__ partials,
+                                                                      const PartDesc* __restrict__ descs) {
+  constexpr int LPR = D / 4;
+  constexpr int kGroups = kJoinThreads / LPR;
+  __shared__ float4 acc[kJoinThreads];
+  __shared__ float acc_l[kGroups], acc_m[kGroups];
   const int w = blockIdx.x;
   const PartDesc d = descs[w];
+  if (d.rows == 0) return;
+  const int count = d.last - w + 1;
+  int side = 1;
+  while (side < kGroups && side * 4 < count) side *= 2;
+  const int rows_at_once = kGroups / side;
   const size_t slot = (size_t)M * D + 2 * M;
-  const int c4 = threadIdx.x % LPR, p0 = threadIdx.x / LPR;
-  const float vs = a.v_scale && d.rows > 0 ? a.v_scale[d.head] : 1.f;
-  for (int r = blockIdx.y; r < d.rows; r += gridDim.y) {
+  const int c4 = threadIdx.x % LPR, g = threadIdx.x / LPR, p0 = g % side;
+  const float vs = a.v_scale ? a.v_scale[d.head] : 1.f;
+  for (int base = blockIdx.y * rows_at_once; base < d.rows; base += kJoinY * rows_at_once) {
+    const int r = min(base + g / side, d.rows - 1);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = w + p0; p <= d.last; p += PPB) {
-      const float* s = partials + (size_t)(p == w ? 2 * w + 1 : 2 * p) * slot;
-      const float pm = s[(size_t)M * D + r], pl = s[(size_t)M * D + M + r];
-      const float4 v = *reinterpret_cast<const float4*>(s + (size_t)r * D + 4 * c4);
-      const float mn = fmaxf(m, pm);
-      if (pl > 0.f) {   // an empty partial says nothing
-        const float f = __builtin_amdgcn_exp2f(m - mn), g = __builtin_amdgcn_exp2f(pm - mn);
-        m = mn;
-        l = l * f + pl * g;
-        o.x = o.x * f + v.x * g;
-        o.y = o.y * f + v.y * g;
-        o.z = o.z * f + v.z * g;
-        o.w = o.w * f + v.w * g;
-      }
-    }
-    acc[threadIdx.x] = o;
-    if (c4 == 0) {
-      acc_m[p0] = m;
-      acc_l[p0] = l;
-    }
-    __syncthreads();
-    if (p0 == 0) {
-      float mx = -INFINITY;
+    for (int p = p0; p < count; p += 4 * side) {
+      float pm[4], pl[4];
+      float4 v[4];
 #pragma unroll
-      for (int i = 0; i < PPB; ++i) mx = fmaxf(mx, acc_m[i]);
-      float sum = 0.f, v0 = 0.f, v1 = 0.f, v2 = 0.f, v3 = 0.f;
-#pragma unroll
-      for (int i = 0; i < PPB; ++i) {
-        const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(acc_m[i] - mx);
-        const float4 v = acc[i * LPR + c4];
-        sum += f * acc_l[i];
-        v0 += f * v.x; v1 += f * v.y; v2 += f * v.z; v3 += f * v.w;
+      for (int i = 0; i < 4; ++i) {
+        const int at = w + min(p + i * side, count - 1);
+        const float* s = partials + (size_t)(at == w ? 2 * w + 1 : 2 * at) * slot;
+        pm[i] = s[(size_t)M * D + r];
+        pl[i] = p + i * side < count ? s[(size_t)M * D + M + r] : 0.f;
+        v[i] = *reinterpret_cast<const float4*>(s + (size_t)r * D + 4 * c4);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (pl[i] > 0.f) {   // an empty partial says nothing
+          const float mn = fmaxf(m, pm[i]);
+          const float f = __builtin_amdgcn_exp2f(m - mn), e = __builtin_amdgcn_exp2f(pm[i] - mn);
+          m = mn;
+          l = l * f + pl[i] * e;
+          o.x = o.x * f + v[i].x * e;
+          o.y = o.y * f + v[i].y * e;
+          o.z = o.z * f + v[i].z * e;
+          o.w = o.w * f + v[i].w * e;
+        }
+    }
+    if (side > 1) {
+      acc[threadIdx.x] = o;
+      if (c4 == 0) {
+        acc_m[g] = m;
+        acc_l[g] = l;
+      }
+      __syncthreads();
+      if (p0 == 0) {
+        float mx = m;
+        for (int i = 1; i < side; ++i) mx = fmaxf(mx, acc_m[g + i]);
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < side; ++i) {
+          const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(acc_m[g + i] - mx);
+          const float4 v = acc[(g + i) * LPR + c4];
+          l += f * acc_l[g + i];
+          o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+        }
+        m = mx;
+      }
+      __syncthreads();
+    }
+    if (p0 == 0 && base + g / side < d.rows) {
       const int tok = r / a.G;
       const size_t at = (size_t)(d.row0 + tok) * a.Hq + d.head * a.G + r - tok * a.G;
-      const float f = sum > 0.f ? vs / sum : 0.f;
+      const float f = l > 0.f ? vs / l : 0.f;
       *reinterpret_cast<uint2*>(a.out + at * D + 4 * c4) =
-          make_uint2(pack_bf16x2(v0 * f, v1 * f), pack_bf16x2(v2 * f, v3 * f));
-      if (a.lse && c4 == 0) a.lse[at] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+          make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+      if (a.lse && c4 == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
-    __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------------------------- the launch
-constexpr int kParts = 256;   // one workgroup per CU
+// Parts of the line of segments = workgroups, all resident at once: one per CU (256), or two where
+// the register file and LDS hold two (128-row tiles of head_dim 64 and 128)
+constexpr int parts_of(int M, int D) { return M == 128 && D < 256 ? 512 : 256; }
 
 // Rows of a workgroup's tile for calls of at most max_q tokens per sequence
 static int tile_rows(int max_q, int G, int D) {
@@ -747,7 +838,8 @@ static size_t slot_floats(int M, int D) { return (size_t)M * D + 2 * M; }
 
 size_t attention_workspace_bytes(int S, int max_q, int Hq, int Hkv, int D) {
   (void)S;
-  return 2 * kParts * slot_floats(tile_rows(max_q, Hq / Hkv, D), D) * 4 + kParts * sizeof(PartDesc);
+  const int M = tile_rows(max_q, Hq / Hkv, D);
+  return parts_of(M, D) * (2 * slot_floats(M, D) * 4 + sizeof(PartDesc));
 }
 
 template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
@@ -757,14 +849,15 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
   if (e != hipSuccess) return e;
+  constexpr int kParts = parts_of(C::M, D);
   float* partials = static_cast<float*>(a.ws);
   PartDesc* descs = reinterpret_cast<PartDesc*>(partials + 2 * kParts * slot_floats(C::M, D));
   hipLaunchKernelGGL(kernel, dim3(kParts), dim3(64 * C::kWaves), C::LDS, stream, a, C::M / a.G, kParts, partials,
                      descs);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(attention_join_kernel<D>, dim3(kParts, C::M / 4), dim3(256), 0, stream, a, C::M,
-                     (const float*)partials, (const PartDesc*)descs);
+  hipLaunchKernelGGL(attention_join_kernel<D>, dim3(kParts, kJoinY), dim3(kJoinThreads), 0, stream, a,
+                     C::M, (const float*)partials, (const PartDesc*)descs);
   return hipGetLastError();
 }
 
