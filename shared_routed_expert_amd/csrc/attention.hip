@@ -117,8 +117,10 @@ __device__ __forceinline__ f16x8 f16_of_e4m3(int a, int b) {
 struct SeqTiles {
   int row0, n, kv, ctx, lo, MT;
   __device__ __forceinline__ int vis(int i, int TB) const { return max(lo, ctx + min(n, (i + 1) * TB)); }
-  // cost of tiles 0..mt-1 of one head: vis + kSegCost each, in closed form
-  __device__ __forceinline__ long cost(int mt, int TB) const {
+  // cost of tiles 0..mt-1 of one head: vis + kSegCost each, in closed form; 1 each where segments are
+  // taken whole
+  __device__ __forceinline__ long cost(int mt, int TB, bool whole) const {
+    if (whole) return mt;
     const long star = lo > ctx ? min(MT, (lo - ctx) / TB) : 0;   // the tiles with ctx + (i + 1) TB <= lo
     long f = (long)mt * kSegCost + min((long)mt, star) * lo;
     if (mt > star) {
@@ -186,9 +188,9 @@ struct Attn {
 
 template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
 __global__ void __launch_bounds__(64 * RW * KW)
-__attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 256 ? 2 : 1))) attention_kernel(const AttnArgs a, const int TB, const int parts_max,
-                                                                 float* __restrict__ partials,
-                                                                 PartDesc* __restrict__ descs) {
+__attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 256 ? 2 : 1))) attention_kernel(
+    const AttnArgs a, const int TB, const int parts_max, const bool whole, float* __restrict__ partials,
+    PartDesc* __restrict__ descs) {
   using C = Attn<D, FP8, QT, RW, KW, NK, CAP>;
   constexpr int kThreads = 64 * C::kWaves;
   extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
@@ -199,8 +201,10 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int rw = wave % RW, kw = wave / RW;
   const int half = lane >> 5, col = lane & 31;
-  // consecutive parts on one XCD: they walk neighbouring keys
-  const int w = (int)(blockIdx.x & 7) * (parts_max >> 3) + (int)(blockIdx.x >> 3);
+  // split: consecutive parts on one XCD, they walk neighbouring keys. Whole: the last tiles of a
+  // sequence, which see the most keys, first.
+  const int w = whole ? parts_max - 1 - (int)blockIdx.x
+                      : (int)(blockIdx.x & 7) * (parts_max >> 3) + (int)(blockIdx.x >> 3);
 
   // -------- which part of the line of segments is this workgroup's
   const int per = (a.S + kThreads - 1) / kThreads;
@@ -208,7 +212,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   long mine = 0;
   for (int s = s_lo; s < s_hi; ++s) {
     const SeqTiles t = seq_tiles(a, s, TB);
-    mine += t.cost(t.MT, TB) * a.Hkv;
+    mine += t.cost(t.MT, TB, whole) * a.Hkv;
   }
   long incl = mine;
 #pragma unroll
@@ -225,9 +229,9 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     total += scan_sum[i];
   }
   total = uni(total);
-  if (tid == 0) descs[w] = PartDesc{0, 0, 0, 0};
+  if (tid == 0 && !whole) descs[w] = PartDesc{0, 0, 0, 0};
   if (total == 0) return;
-  const int parts = (int)min((long)parts_max, (total + kMinPart - 1) / kMinPart);
+  const int parts = (int)min((long)parts_max, whole ? total : (total + kMinPart - 1) / kMinPart);
   if (w >= parts) return;
   const Parts split(total, parts);
   long u = split.begin(w);
@@ -236,7 +240,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     long r = u - before;
     for (int s = s_lo; s < s_hi; ++s) {
       const SeqTiles t = seq_tiles(a, s, TB);
-      const long c = t.cost(t.MT, TB) * a.Hkv;
+      const long c = t.cost(t.MT, TB, whole) * a.Hkv;
       if (r < c) {
         found_seq = s;
         found_rem = r;
@@ -251,17 +255,17 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   SeqTiles seq = uniform_seq(a, s, TB);
   int h, mt;
   {
-    const long per_head = seq.cost(seq.MT, TB);
+    const long per_head = seq.cost(seq.MT, TB, whole);
     h = uni((int)(rem / per_head));
     rem -= h * per_head;
     int lo = 0, hi = seq.MT;   // the largest tile with cost(tile) <= rem
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (seq.cost(mid, TB) <= rem) lo = mid;
+      if (seq.cost(mid, TB, whole) <= rem) lo = mid;
       else hi = mid;
     }
     mt = uni(lo);
-    rem -= seq.cost(mt, TB);
+    rem -= seq.cost(mt, TB, whole);
   }
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)sm;
@@ -291,7 +295,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   while (u < u_end) {
     // -------- the segment: rows, keys, and this part's share of its tiles
     const int vis = seq.vis(mt, TB);
-    const long seg_cost = vis + kSegCost;
+    const long seg_cost = whole ? 1 : vis + kSegCost;
     const long seg_end = u - rem + seg_cost;
     const bool begins = rem == 0, ends = seg_end <= u_end;
     const int ntiles = (vis + NK - 1) / NK;
@@ -829,6 +833,9 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 // the register file and LDS hold two (128-row tiles of head_dim 64 and 128)
 constexpr int parts_of(int M, int D) { return M == 128 && D < 256 ? 512 : 256; }
 
+// From this many segments on, one workgroup takes a whole one
+constexpr long kWholeSegments = 1536;
+
 // Rows of a workgroup's tile for calls of at most max_q tokens per sequence
 static int tile_rows(int max_q, int G, int D) {
   const long rows = (long)max_q * G;
@@ -852,7 +859,15 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   constexpr int kParts = parts_of(C::M, D);
   float* partials = static_cast<float*>(a.ws);
   PartDesc* descs = reinterpret_cast<PartDesc*>(partials + 2 * kParts * slot_floats(C::M, D));
-  hipLaunchKernelGGL(kernel, dim3(kParts), dim3(64 * C::kWaves), C::LDS, stream, a, C::M / a.G, kParts, partials,
+  const int TB = C::M / a.G;
+  // at least this many segments, by the rows of q alone (a device-side count would come too late)
+  const long segments = (long)a.Hkv * (a.T / TB);
+  if (KW == 1 && segments >= kWholeSegments) {
+    const int grid = (int)((long)a.Hkv * ((a.T + TB - 1) / TB + a.S));
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, true, partials, descs);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(kernel, dim3(kParts), dim3(64 * C::kWaves), C::LDS, stream, a, TB, kParts, false, partials,
                      descs);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
