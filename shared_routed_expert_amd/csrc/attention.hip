@@ -48,7 +48,6 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kMoveMax = 8.0f;    // a running maximum moves when a score exceeds it by this (base 2)
 constexpr int kSegCost = 64;        // a segment's fixed cost, in keys, for the work split
-constexpr int kMinPart = 256;       // a part holds at least this many keys' cost
 
 // 16-byte chunk swap of key k's row (CPR chunks of it), for LDS's 64 banks of 4 bytes: 16 consecutive
 // keys' same chunk (a step of K's reads) and the 64 or 32 bytes of {4h..4h+3} (8-bit: and 8+4h..) of a
@@ -142,25 +141,31 @@ __device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, int s, int TB) 
   return t;
 }
 
-// the same for a sequence that is one for the whole wave, held in scalar registers
-__device__ __forceinline__ SeqTiles uniform_seq(const AttnArgs& a, int s, int TB) {
-  SeqTiles t = seq_tiles(a, s, TB);
+// a sequence that is the same for the whole wave, in scalar registers
+__device__ __forceinline__ SeqTiles uniform(SeqTiles t) {
   t.row0 = uni(t.row0); t.n = uni(t.n); t.kv = uni(t.kv); t.ctx = uni(t.ctx); t.lo = uni(t.lo); t.MT = uni(t.MT);
   return t;
 }
 
-struct PartDesc {   // a segment that begins in part w and ends in a later part `last`
-  int row0, rows, head, last;
+// A segment that begins in part `first` and ends in a later part `last` (rows == 0: nothing to join)
+struct alignas(32) PartDesc {
+  int row0, rows, head, first, last;
 };
+
+// a / b for a >= 0, b > 0: in 32 bits where they fit (a 64-bit division costs over a hundred instructions)
+__device__ __forceinline__ long div_pos(long a, long b) {
+  if (((uint64_t)(a | b) >> 32) == 0) return (long)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
 
 // Part w of `parts` covers [begin(w), begin(w + 1)) of `total` units.
 struct Parts {
   long q, rem;
-  __device__ __forceinline__ Parts(long total, int parts) : q(total / parts), rem(total % parts) {}
+  __device__ __forceinline__ Parts(long total, int parts) : q(div_pos(total, parts)), rem(total - q * parts) {}
   __device__ __forceinline__ long begin(int w) const { return q * w + min((long)w, rem); }
   __device__ __forceinline__ int of(long unit) const {   // the part that holds a unit
     const long big = (q + 1) * rem;
-    return (int)(unit < big ? unit / (q + 1) : rem + (unit - big) / q);
+    return (int)(unit < big ? div_pos(unit, q + 1) : rem + div_pos(unit - big, q));
   }
 };
 
@@ -181,6 +186,7 @@ struct Attn {
   static constexpr int KT = NK / 32;            // 32-key tiles of scores
   static constexpr int DT = D / 32;
   static constexpr int STEPS = D / 16;
+  static constexpr int kMinPart = RW == 1 ? KW * NK : 4 * NK;   // a part's cost in keys is at least this
   static constexpr int SLOT = M * D + 2 * M;    // floats of a partial: O [M][D], then m and l per row
   static_assert(NX % RW == 0 && RPI <= 16 && NK <= 64, "tile shape");
   static_assert(KW == 1 || M * D * 4 <= 2 * STAGE, "the waves' sums are joined in their stages");
@@ -189,14 +195,15 @@ struct Attn {
 template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
 __global__ void __launch_bounds__(64 * RW * KW)
 __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 256 ? 2 : 1))) attention_kernel(
-    const AttnArgs a, const int TB, const int parts_max, const bool whole, float* __restrict__ partials,
-    PartDesc* __restrict__ descs) {
+    const AttnArgs a, const int TB, const int parts_max, const bool whole, const int desc_tiles,
+    float* __restrict__ partials, PartDesc* __restrict__ descs) {
   using C = Attn<D, FP8, QT, RW, KW, NK, CAP>;
   constexpr int kThreads = 64 * C::kWaves;
   extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
   __shared__ long scan_sum[C::kWaves];
   __shared__ long found_rem;
-  __shared__ int found_seq;
+  __shared__ int found_s;
+  __shared__ SeqTiles found_seq;
   __shared__ float row_m[KW][C::M], row_l[KW][C::M];
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int rw = wave % RW, kw = wave / RW;
@@ -229,9 +236,9 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     total += scan_sum[i];
   }
   total = uni(total);
-  if (tid == 0 && !whole) descs[w] = PartDesc{0, 0, 0, 0};
+  if (tid == 0 && !whole && desc_tiles == 0) descs[w] = PartDesc{0, 0, 0, 0, 0};
   if (total == 0) return;
-  const int parts = (int)min((long)parts_max, whole ? total : (total + kMinPart - 1) / kMinPart);
+  const int parts = (int)min((long)parts_max, whole ? total : (total + C::kMinPart - 1) / C::kMinPart);
   if (w >= parts) return;
   const Parts split(total, parts);
   long u = split.begin(w);
@@ -242,7 +249,8 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
       const SeqTiles t = seq_tiles(a, s, TB);
       const long c = t.cost(t.MT, TB, whole) * a.Hkv;
       if (r < c) {
-        found_seq = s;
+        found_s = s;
+        found_seq = t;
         found_rem = r;
         break;
       }
@@ -250,13 +258,13 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     }
   }
   __syncthreads();
-  int s = uni(found_seq);
+  int s = uni(found_s);
   long rem = uni(found_rem);
-  SeqTiles seq = uniform_seq(a, s, TB);
+  SeqTiles seq = uniform(found_seq);
   int h, mt;
   {
     const long per_head = seq.cost(seq.MT, TB, whole);
-    h = uni((int)(rem / per_head));
+    h = uni((int)div_pos(rem, per_head));
     rem -= h * per_head;
     int lo = 0, hi = seq.MT;   // the largest tile with cost(tile) <= rem
     while (hi - lo > 1) {
@@ -311,54 +319,17 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     const uint8_t* const kc = static_cast<const uint8_t*>(a.k_cache) + ((size_t)h << a.page_shift) * C::RB;
     const uint8_t* const vc = static_cast<const uint8_t*>(a.v_cache) + ((size_t)h << a.page_shift) * C::RB;
 
-    bf16x8 q[QT][C::STEPS];
-    int lim[QT];
-    uint64_t word[QT];
-#pragma unroll
-    for (int x = 0; x < QT; ++x) {
-      // rows past the tile's last repeat it and are not stored
-      const int r = min((rw * QT + x) * 32 + col, rows - 1);
-      const int tok = r / a.G, qrow = row0 + tok;
-      const uint16_t* p = a.q + (size_t)qrow * a.q_stride + (size_t)(h * a.G + r - tok * a.G) * D;
-#pragma unroll
-      for (int st = 0; st < C::STEPS; ++st) {
-        const int d = FP8 ? 32 * (st >> 1) + 16 * half + 8 * (st & 1) : 16 * st + 8 * half;
-        q[x][st] = *reinterpret_cast<const bf16x8*>(p + d);
-      }
-      if (a.tree_mask) {
-        lim[x] = max(seq.ctx, 0);
-        word[x] = a.tree_mask[qrow] & (~0ull >> (64 - seq.n));
-      } else {
-        lim[x] = max(seq.lo, seq.ctx + tok0 + tok + 1);
-        word[x] = 0;
-      }
-    }
-    // q is here before the key loop: a wait for it inside would wait for the tiles in flight too
-#pragma unroll
-    for (int x = 0; x < QT; ++x)
-#pragma unroll
-      for (int st = 0; st < C::STEPS; ++st) asm volatile("" ::"v"(__builtin_bit_cast(i32x4, q[x][st])));
-    // keys below this are seen by every row
-    const int all_see = a.tree_mask ? max(seq.ctx, 0) : max(seq.lo, seq.ctx + tok0 + 1);
-
-    v16f o[QT][C::DT];
-    float m[QT], l[QT];
-#pragma unroll
-    for (int x = 0; x < QT; ++x) {
-      m[x] = -INFINITY;
-      l[x] = 0.f;
-#pragma unroll
-      for (int d = 0; d < C::DT; ++d) o[x][d] = v16f{};
-    }
+    // this wave's tiles: all of the part's (shared), or a stretch of its own
+    const int wt0 = RW == 1 ? t0 + (int)((long)(t1 - t0) * kw / KW) : t0;
+    const int wt1 = RW == 1 ? t0 + (int)((long)(t1 - t0) * (kw + 1) / KW) : t1;
 
     // -------- page ids: 64 at a time, one per lane; pages outside the pool (and past the last
     // cached token) are read as page 0 and masked
     int pg = 0, pg_base = -64;
     bool careful = false;   // a page outside the pool was met
-    auto refill = [&](int first) {
+    auto fetch_ids = [&](int first) { return first + lane < pages_used ? table[first + lane] : 0; };
+    auto take_ids = [&](int first, int id) {
       pg_base = first;
-      const int i = first + lane;
-      const int id = i < pages_used ? table[i] : 0;
       const bool bad = id < 0 || id >= a.num_pages;
       careful = careful || __ballot(bad) != 0;
       pg = bad ? 0 : id;
@@ -370,7 +341,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     // a tile's keys lie in pages [key0 >> shift, (key0 + NK - 1) >> shift]: at most 4 of them
     auto pages_for = [&](int key0) {
       const int i = key0 >> a.page_shift;
-      if (i + (NK - 1) / 16 >= pg_base + 64 || i < pg_base) refill(i);
+      if (i + (NK - 1) / 16 >= pg_base + 64) take_ids(i, fetch_ids(i));
     };
     auto issue = [&](const uint8_t* cache, uint32_t lds, int key0) {
 #pragma unroll
@@ -399,6 +370,51 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
           *reinterpret_cast<uint4*>(v + x * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
       }
     };
+
+    const int first_page = wt0 * NK >> a.page_shift;
+    const int first_ids = fetch_ids(first_page);
+    bf16x8 q[QT][C::STEPS];
+    int lim[QT];
+    uint64_t word[QT];
+#pragma unroll
+    for (int x = 0; x < QT; ++x) {
+      // rows past the tile's last repeat it and are not stored
+      const int r = min((rw * QT + x) * 32 + col, rows - 1);
+      const int tok = r / a.G, qrow = row0 + tok;
+      const uint16_t* p = a.q + (size_t)qrow * a.q_stride + (size_t)(h * a.G + r - tok * a.G) * D;
+#pragma unroll
+      for (int st = 0; st < C::STEPS; ++st) {
+        const int d = FP8 ? 32 * (st >> 1) + 16 * half + 8 * (st & 1) : 16 * st + 8 * half;
+        q[x][st] = *reinterpret_cast<const bf16x8*>(p + d);
+      }
+      if (a.tree_mask) {
+        lim[x] = max(seq.ctx, 0);
+        word[x] = a.tree_mask[qrow] & (~0ull >> (64 - seq.n));
+      } else {
+        lim[x] = max(seq.lo, seq.ctx + tok0 + tok + 1);
+        word[x] = 0;
+      }
+    }
+    take_ids(first_page, first_ids);
+    // q is here before the key loop: a wait for it inside would wait for the tiles in flight too
+    auto wait_q = [&]() {
+#pragma unroll
+      for (int x = 0; x < QT; ++x)
+#pragma unroll
+        for (int st = 0; st < C::STEPS; ++st) asm volatile("" ::"v"(__builtin_bit_cast(i32x4, q[x][st])));
+    };
+    // keys below this are seen by every row
+    const int all_see = a.tree_mask ? max(seq.ctx, 0) : max(seq.lo, seq.ctx + tok0 + 1);
+
+    v16f o[QT][C::DT];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int x = 0; x < QT; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+#pragma unroll
+      for (int d = 0; d < C::DT; ++d) o[x][d] = v16f{};
+    }
 
     // -------- scores of one key tile. Each product's operand is read from LDS kAhead products
     // earlier, and the fences keep that order: left alone, the compiler reads right before use and every
@@ -575,14 +591,13 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
       // (after the scores of tile 0) V2 (after its values) ..., so with L = NX loads per tile the
       // ones younger than K_t are V_t K_t+1 V_t+1, and those younger than V_t K_t+1 V_t+1 K_t+2
       constexpr int L = C::NX;
-      const int cnt = t1 - t0;
-      const int wt0 = t0 + (int)((long)cnt * kw / KW), wt1 = t0 + (int)((long)cnt * (kw + 1) / KW);
       for (int t = wt0; t < min(wt0 + 2, wt1); ++t) {
         const uint32_t st = stages_off + ((t - wt0) & 1) * C::STAGE;
         pages_for(t * NK);
         issue(kc, st, t * NK);
         issue(vc, st + C::TILE, t * NK);
       }
+      wait_q();
       for (int t = wt0; t < wt1; ++t) {
         const int b = (t - wt0) & 1, left = wt1 - 1 - t;
         uint8_t* const st = stages + b * C::STAGE;
@@ -619,6 +634,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
         issue(kc, stages_off, t0 * NK);
         issue(vc, stages_off + C::TILE, t0 * NK);
       }
+      wait_q();
       for (int t = t0; t < t1; ++t) {
         const int b = (t - t0) & 1;
         uint8_t* const st = stages + b * C::STAGE;
@@ -642,7 +658,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     }
 
     // -------- the segment's result, or this part's partial
-    const bool whole = begins && ends;
+    const bool complete = begins && ends;
     float* const slot = partials + (size_t)(2 * w + (begins ? 1 : 0)) * C::SLOT;
     const float vs = FP8 ? a.v_scale[h] : 1.f;
     if constexpr (KW == 1) {
@@ -651,7 +667,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
         const int r = (rw * QT + x) * 32 + col;
         const float sum = swap_sum(l[x]);
         if (r < rows) {
-          if (whole) {
+          if (complete) {
             const int tok = r / a.G, head = h * a.G + r - tok * a.G;
             const size_t at = (size_t)(row0 + tok) * a.Hq + head;
             const float f = sum > 0.f ? vs / sum : 0.f;
@@ -710,7 +726,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
           sum += f * row_l[k][r];
           v0 += f * v.x; v1 += f * v.y; v2 += f * v.z; v3 += f * v.w;
         }
-        if (whole) {
+        if (complete) {
           const int tok = r / a.G, head = h * a.G + r - tok * a.G;
           const size_t at = (size_t)(row0 + tok) * a.Hq + head;
           const float f = sum > 0.f ? vs / sum : 0.f;
@@ -727,7 +743,13 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
       }
       __syncthreads();   // the stages are free again
     }
-    if (begins && !ends && tid == 0) descs[w] = PartDesc{row0, rows, h, split.of(seg_end - 1)};
+    if (begins && tid == 0 && !whole) {
+      if (desc_tiles > 0)
+        descs[((size_t)s * a.Hkv + h) * desc_tiles + mt] =
+            PartDesc{row0, ends ? 0 : rows, h, w, ends ? w : split.of(seg_end - 1)};
+      else if (!ends)
+        descs[w] = PartDesc{row0, rows, h, w, split.of(seg_end - 1)};
+    }
 
     // -------- the next segment
     u = min(u_end, seg_end);
@@ -736,38 +758,43 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
       mt = 0;
       if (++h >= a.Hkv && u < u_end) {
         h = 0;
-        do seq = uniform_seq(a, ++s, TB);
+        do seq = uniform(seq_tiles(a, ++s, TB));
         while (seq.n == 0);
       }
     }
   }
 }
 
-// Joins the partials of segments that span several parts: workgroup (w, y) takes rows of the
-// segment that begins in part w. D / 4 lanes read a partial's row (16 bytes each); the workgroup's
+// Joins the partials of segments that span several parts: workgroup (i, y) takes rows of the
+// segment of description i. There is one description per segment, or, where that would be many, one per
+// part for the segment that begins in it and goes on. D / 4 lanes read a partial's row (16 bytes each); the workgroup's
 // groups of such lanes stand side by side on `side` partials of a row (few partials: on rows of
 // their own), and each has 4 partials in flight, so that neither a segment split over the whole card
 // nor 128 rows of two partials each wait for memory more than a few times.
-constexpr int kJoinThreads = 512, kJoinY = 8;
+constexpr int kJoinThreads = 512;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, const int M,
+                                                                      const int TB, const int desc_tiles,
                                                                       const float* __restrict__ partials,
                                                                       const PartDesc* __restrict__ descs) {
   constexpr int LPR = D / 4;
   constexpr int kGroups = kJoinThreads / LPR;
   __shared__ float4 acc[kJoinThreads];
   __shared__ float acc_l[kGroups], acc_m[kGroups];
-  const int w = blockIdx.x;
-  const PartDesc d = descs[w];
+  const PartDesc d = descs[blockIdx.x];
+  if (desc_tiles > 0) {   // a tile that its sequence does not have has no description
+    const int s = (int)blockIdx.x / (desc_tiles * a.Hkv), mt = (int)blockIdx.x % desc_tiles;
+    if (mt * TB >= seq_info(a, s).n) return;
+  }
   if (d.rows == 0) return;
-  const int count = d.last - w + 1;
+  const int w = d.first, count = d.last - w + 1;
   int side = 1;
   while (side < kGroups && side * 4 < count) side *= 2;
   const int rows_at_once = kGroups / side;
   const size_t slot = (size_t)M * D + 2 * M;
   const int c4 = threadIdx.x % LPR, g = threadIdx.x / LPR, p0 = g % side;
   const float vs = a.v_scale ? a.v_scale[d.head] : 1.f;
-  for (int base = blockIdx.y * rows_at_once; base < d.rows; base += kJoinY * rows_at_once) {
+  for (int base = blockIdx.y * rows_at_once; base < d.rows; base += gridDim.y * rows_at_once) {
     const int r = min(base + g / side, d.rows - 1);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -846,7 +873,7 @@ static size_t slot_floats(int M, int D) { return (size_t)M * D + 2 * M; }
 size_t attention_workspace_bytes(int S, int max_q, int Hq, int Hkv, int D) {
   (void)S;
   const int M = tile_rows(max_q, Hq / Hkv, D);
-  return parts_of(M, D) * (2 * slot_floats(M, D) * 4 + sizeof(PartDesc));
+  return parts_of(M, D) * 2 * (slot_floats(M, D) * 4 + sizeof(PartDesc));
 }
 
 template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
@@ -864,15 +891,22 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   const long segments = (long)a.Hkv * (a.T / TB);
   if (KW == 1 && segments >= kWholeSegments) {
     const int grid = (int)((long)a.Hkv * ((a.T + TB - 1) / TB + a.S));
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, true, partials, descs);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, true, 0, partials,
+                       descs);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(kernel, dim3(kParts), dim3(64 * C::kWaves), C::LDS, stream, a, TB, kParts, false, partials,
-                     descs);
+  const int tiles = (a.max_q + TB - 1) / TB;
+  const long most = (long)a.S * a.Hkv * tiles;   // segments, if every sequence had max_q tokens
+  const bool by_segment = most <= 2 * kParts;
+  hipLaunchKernelGGL(kernel, dim3(kParts), dim3(64 * C::kWaves), C::LDS, stream, a, TB, kParts, false,
+                     by_segment ? tiles : 0, partials, descs);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(attention_join_kernel<D>, dim3(kParts, kJoinY), dim3(kJoinThreads), 0, stream, a,
-                     C::M, (const float*)partials, (const PartDesc*)descs);
+  // about as many workgroups as are resident at once, and no more than a segment has rows
+  const int rows = (int)min((long)C::M, (long)a.max_q * a.G);
+  const int y = by_segment ? max(1, min((int)(1024 / most), min(rows, 16))) : 2;
+  hipLaunchKernelGGL(attention_join_kernel<D>, dim3(by_segment ? (int)most : kParts, y), dim3(kJoinThreads), 0,
+                     stream, a, C::M, TB, by_segment ? tiles : 0, (const float*)partials, (const PartDesc*)descs);
   return hipGetLastError();
 }
 
