@@ -767,29 +767,17 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
 
 // Joins the partials of segments that span several parts: workgroup (i, y) takes rows of the
 // segment of description i. There is one description per segment, or, where that would be many, one per
-// part for the segment that begins in it and goes on. D / 4 lanes read a partial's row (16 bytes each); the workgroup's
-// groups of such lanes stand side by side on `side` partials of a row (few partials: on rows of
-// their own), and each has 4 partials in flight, so that neither a segment split over the whole card
-// nor 128 rows of two partials each wait for memory more than a few times.
-constexpr int kJoinThreads = 512;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, const int M,
-                                                                      const int TB, const int desc_tiles,
-                                                                      const float* __restrict__ partials,
-                                                                      const PartDesc* __restrict__ descs) {
+// part for the segment that begins in it and goes on. D / 4 lanes read a partial's row (16 bytes
+// each); the workgroup's groups of such lanes stand side by side on `side` partials of a row (few
+// partials: on rows of their own), and each has kBatch of them in flight, so that neither a segment
+// split over the whole card nor 128 rows of two partials each wait for memory more than a few times.
+constexpr int kJoinThreads = 256;
+template <int D, int kBatch>
+__device__ __forceinline__ void join_rows(const AttnArgs& a, const int M, const PartDesc& d, const int side,
+                                          const float* __restrict__ partials, float4* acc, float* acc_l, float* acc_m) {
   constexpr int LPR = D / 4;
   constexpr int kGroups = kJoinThreads / LPR;
-  __shared__ float4 acc[kJoinThreads];
-  __shared__ float acc_l[kGroups], acc_m[kGroups];
-  const PartDesc d = descs[blockIdx.x];
-  if (desc_tiles > 0) {   // a tile that its sequence does not have has no description
-    const int s = (int)blockIdx.x / (desc_tiles * a.Hkv), mt = (int)blockIdx.x % desc_tiles;
-    if (mt * TB >= seq_info(a, s).n) return;
-  }
-  if (d.rows == 0) return;
   const int w = d.first, count = d.last - w + 1;
-  int side = 1;
-  while (side < kGroups && side * 4 < count) side *= 2;
   const int rows_at_once = kGroups / side;
   const size_t slot = (size_t)M * D + 2 * M;
   const int c4 = threadIdx.x % LPR, g = threadIdx.x / LPR, p0 = g % side;
@@ -798,11 +786,11 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     const int r = min(base + g / side, d.rows - 1);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = p0; p < count; p += 4 * side) {
-      float pm[4], pl[4];
-      float4 v[4];
+    for (int p = p0; p < count; p += kBatch * side) {
+      float pm[kBatch], pl[kBatch];
+      float4 v[kBatch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kBatch; ++i) {
         const int at = w + min(p + i * side, count - 1);
         const float* s = partials + (size_t)(at == w ? 2 * w + 1 : 2 * at) * slot;
         pm[i] = s[(size_t)M * D + r];
@@ -810,7 +798,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         v[i] = *reinterpret_cast<const float4*>(s + (size_t)r * D + 4 * c4);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kBatch; ++i)
         if (pl[i] > 0.f) {   // an empty partial says nothing
           const float mn = fmaxf(m, pm[i]);
           const float f = __builtin_amdgcn_exp2f(m - mn), e = __builtin_amdgcn_exp2f(pm[i] - mn);
@@ -853,6 +841,28 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
       if (a.lse && c4 == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, const int M, const int TB,
+                                                                      const int desc_tiles,
+                                                                      const float* __restrict__ partials,
+                                                                      const PartDesc* __restrict__ descs) {
+  constexpr int kGroups = kJoinThreads / (D / 4);
+  __shared__ float4 acc[kJoinThreads];
+  __shared__ float acc_l[kGroups], acc_m[kGroups];
+  const PartDesc d = descs[blockIdx.x];
+  if (desc_tiles > 0) {   // a tile that its sequence does not have has no description
+    const int s = (int)blockIdx.x / (desc_tiles * a.Hkv), mt = (int)blockIdx.x % desc_tiles;
+    if (mt * TB >= seq_info(a, s).n) return;
+  }
+  if (d.rows == 0) return;
+  const int count = d.last - d.first + 1;
+  int side = 1;
+  while (side < kGroups && side * 8 < count) side *= 2;
+  if (count <= 2) join_rows<D, 2>(a, M, d, side, partials, acc, acc_l, acc_m);
+  else if (count <= 4) join_rows<D, 4>(a, M, d, side, partials, acc, acc_l, acc_m);
+  else join_rows<D, 8>(a, M, d, side, partials, acc, acc_l, acc_m);
 }
 
 // ------------------------------------------------------------------------------------- the launch
@@ -904,7 +914,7 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   // about as many workgroups as are resident at once, and no more than a segment has rows
   const int rows = (int)min((long)C::M, (long)a.max_q * a.G);
-  const int y = by_segment ? max(1, min((int)(1024 / most), min(rows, 16))) : 2;
+  const int y = by_segment ? max(1, min((int)(2048 / most), min(rows, 32))) : 4;
   hipLaunchKernelGGL(attention_join_kernel<D>, dim3(by_segment ? (int)most : kParts, y), dim3(kJoinThreads), 0,
                      stream, a, C::M, TB, by_segment ? tiles : 0, (const float*)partials, (const PartDesc*)descs);
   return hipGetLastError();
