@@ -208,11 +208,6 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int rw = wave % RW, kw = wave / RW;
   const int half = lane >> 5, col = lane & 31;
-  // split: consecutive parts on one XCD, they walk neighbouring keys. Whole: the last tiles of a
-  // sequence, which see the most keys, first.
-  const int w = whole ? parts_max - 1 - (int)blockIdx.x
-                      : (int)(blockIdx.x & 7) * (parts_max >> 3) + (int)(blockIdx.x >> 3);
-
   // -------- which part of the line of segments is this workgroup's
   const int per = (a.S + kThreads - 1) / kThreads;
   const int s_lo = min(tid * per, a.S), s_hi = min(s_lo + per, a.S);
@@ -236,10 +231,16 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     total += scan_sum[i];
   }
   total = uni(total);
-  if (tid == 0 && !whole && desc_tiles == 0) descs[w] = PartDesc{0, 0, 0, 0, 0};
-  if (total == 0) return;
   const int parts = (int)min((long)parts_max, whole ? total : (total + C::kMinPart - 1) / C::kMinPart);
-  if (w >= parts) return;
+  // Split: consecutive parts on one XCD (they walk neighbouring keys), however many there are on all
+  // XCDs alike. Whole: the last tiles of a sequence, which see the most keys, first.
+  const int w = whole ? parts_max - 1 - (int)blockIdx.x : xcd_tile((int)blockIdx.x, parts);
+  if (!whole && desc_tiles == 0) {   // no segment begins in these parts until one is written below
+    if (blockIdx.x == 0)
+      for (int i = parts + tid; i < parts_max; i += kThreads) descs[i] = PartDesc{0, 0, 0, 0, 0};
+    if (w >= 0 && tid == 0) descs[w] = PartDesc{0, 0, 0, 0, 0};
+  }
+  if (w < 0 || w >= parts) return;
   const Parts split(total, parts);
   long u = split.begin(w);
   const long u_end = split.begin(w + 1);
