@@ -267,13 +267,14 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     const long per_head = seq.cost(seq.MT, TB, whole);
     h = uni((int)div_pos(rem, per_head));
     rem -= h * per_head;
-    int lo = 0, hi = seq.MT;   // the largest tile with cost(tile) <= rem
+    int lo = 0, hi = seq.MT;   // the largest tile with cost(tile) <= rem, 64 candidates at a time
     while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (seq.cost(mid, TB, whole) <= rem) lo = mid;
-      else hi = mid;
+      const int step = (hi - lo + 63) >> 6, at = lo + lane * step;
+      const int n = __popcll(__ballot(at < hi && seq.cost(at, TB, whole) <= rem));
+      lo = uni(lo + (n - 1) * step);
+      hi = uni(min(hi, lo + step));
     }
-    mt = uni(lo);
+    mt = lo;
     rem -= seq.cost(mt, TB, whole);
   }
 
@@ -312,7 +313,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     const int t1 = ends ? ntiles : min(ntiles, (int)((rem + u_end - u) / NK));
     const int tok0 = mt * TB, rows = min(TB, seq.n - tok0) * a.G;
     const int row0 = seq.row0 + tok0;
-    const float ks = FP8 ? a.k_scale[h] : 1.f;
+    const float ks = FP8 ? a.k_scale[h] : 1.f, vs = FP8 ? a.v_scale[h] : 1.f;
     const float c = CAP ? 2.f * kLog2e * a.scale * ks / a.softcap : scale2 * ks;
     const float cap2 = a.softcap * kLog2e;
     const int* table = a.block_table + (size_t)s * a.max_pages;
@@ -661,7 +662,6 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     // -------- the segment's result, or this part's partial
     const bool complete = begins && ends;
     float* const slot = partials + (size_t)(2 * w + (begins ? 1 : 0)) * C::SLOT;
-    const float vs = FP8 ? a.v_scale[h] : 1.f;
     if constexpr (KW == 1) {
 #pragma unroll
       for (int x = 0; x < QT; ++x) {
