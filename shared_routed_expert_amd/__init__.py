@@ -22,12 +22,12 @@ _CACHE = ("PagedKVCache",)
 
 def __getattr__(name):
     if name in _BINDING:
-        from . import _lib
-        return getattr(_lib, name)
-    if name in _LAYER:
-        from . import layer
-        return getattr(layer, name)
-    if name in _CACHE:
-        from . import cache
-        return getattr(cache, name)
-    raise AttributeError(name)
+        from . import _lib as module
+    elif name in _LAYER:
+        from . import layer as module
+    elif name in _CACHE:
+        from . import cache as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)   # found without this function from now on
+    return value

@@ -100,17 +100,20 @@ EXPORTED = ("moe_route_topk_plus_shared", "moe_align_by_expert", "moe_fused_ffn"
 
 def _ptr(t):
     """Device pointer of a tensor, or an int / None passed through (raw pointers in tests)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
+
+
+_raw_stream = None   # torch's current stream of a device as a hipStream_t, without building a Stream object
 
 
 def _stream(stream):
     if stream is None:
+        global _raw_stream
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -896,9 +896,6 @@ template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
 static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   using C = Attn<D, FP8, QT, RW, KW, NK, CAP>;
   auto* kernel = attention_kernel<D, FP8, QT, RW, KW, NK, CAP>;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
-  if (e != hipSuccess) return e;
   constexpr int kParts = parts_of(C::M, D);
   float* partials = static_cast<float*>(a.ws);
   PartDesc* descs = reinterpret_cast<PartDesc*>(partials + 2 * kParts * slot_floats(C::M, D));
@@ -916,7 +913,7 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   const bool by_segment = most <= 2 * kParts;
   hipLaunchKernelGGL(kernel, dim3(kParts), dim3(64 * C::kWaves), C::LDS, stream, a, TB, kParts, false,
                      by_segment ? tiles : 0, partials, descs);
-  e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // about as many workgroups as are resident at once, and no more than a segment has rows
   const int rows = (int)min((long)C::M, (long)a.max_q * a.G);
