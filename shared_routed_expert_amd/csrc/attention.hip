@@ -2,7 +2,7 @@
 // prompt chunks alike.
 //
 // Rows. The query heads that share a kv head read the same keys, so a tile's rows are (token,
-// head of the group) pairs: TB = M / G tokens of a sequence times its G heads, M = 32 QT RW rows.
+// head of the group) pairs: TB = M / G tokens of a sequence times its G heads, M = 32 RW rows.
 // A segment is one such tile against all keys it sees. Row r of a tile sees key j when j <
 // lim_r, or when j is a drafted token whose bit is set in the row's mask word; causal order, a
 // prefix and a tree are all of this form.
@@ -170,10 +170,10 @@ struct Parts {
 };
 
 // -------------------------------------------------------------------------------------- the kernel
-template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
+template <int D, bool FP8, int RW, int KW, int NK, bool CAP>
 struct Attn {
   static constexpr int kWaves = RW * KW;
-  static constexpr int M = 32 * QT * RW;
+  static constexpr int M = 32 * RW;
   static constexpr int ES = FP8 ? 1 : 2;
   static constexpr int RB = D * ES;             // bytes of a key's row
   static constexpr int CPR = RB / 16;           // its 16-byte chunks
@@ -186,18 +186,22 @@ struct Attn {
   static constexpr int KT = NK / 32;            // 32-key tiles of scores
   static constexpr int DT = D / 32;
   static constexpr int STEPS = D / 16;
+  // bf16 weights are split in two (16 bits of them) where memory sets the pace and the second product is
+  // free (decode of 64 sequences takes as long, its error is 0.0017 of the output instead of 0.0023, that of the
+  // output's own rounding). Tiles of more rows round them once (5 drafted tokens of 12 heads: 53 us, split 57).
+  static constexpr bool kSplit = !FP8 && RW == 1;
   static constexpr int kMinPart = RW == 1 ? KW * NK : 4 * NK;   // a part's cost in keys is at least this
   static constexpr int SLOT = M * D + 2 * M;    // floats of a partial: O [M][D], then m and l per row
   static_assert(NX % RW == 0 && RPI <= 16 && NK <= 64, "tile shape");
   static_assert(KW == 1 || M * D * 4 <= 2 * STAGE, "the waves' sums are joined in their stages");
 };
 
-template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
+template <int D, bool FP8, int RW, int KW, int NK, bool CAP>
 __global__ void __launch_bounds__(64 * RW * KW)
 __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 256 ? 2 : 1))) attention_kernel(
     const AttnArgs a, const int TB, const int parts_max, const bool whole, const int desc_tiles,
     float* __restrict__ partials, PartDesc* __restrict__ descs) {
-  using C = Attn<D, FP8, QT, RW, KW, NK, CAP>;
+  using C = Attn<D, FP8, RW, KW, NK, CAP>;
   constexpr int kThreads = 64 * C::kWaves;
   extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
   __shared__ long scan_sum[C::kWaves];
@@ -375,58 +379,46 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
 
     const int first_page = wt0 * NK >> a.page_shift;
     const int first_ids = fetch_ids(first_page);
-    bf16x8 q[QT][C::STEPS];
-    int lim[QT];
-    uint64_t word[QT];
+    bf16x8 q[C::STEPS];
+    int lim;
+    uint64_t word;
+    // rows past the tile's last repeat it and are not stored
+    const int r = min(rw * 32 + col, rows - 1);
+    const int tok = r / a.G, qrow = row0 + tok;
+    const uint16_t* p = a.q + (size_t)qrow * a.q_stride + (size_t)(h * a.G + r - tok * a.G) * D;
 #pragma unroll
-    for (int x = 0; x < QT; ++x) {
-      // rows past the tile's last repeat it and are not stored
-      const int r = min((rw * QT + x) * 32 + col, rows - 1);
-      const int tok = r / a.G, qrow = row0 + tok;
-      const uint16_t* p = a.q + (size_t)qrow * a.q_stride + (size_t)(h * a.G + r - tok * a.G) * D;
-#pragma unroll
-      for (int st = 0; st < C::STEPS; ++st) {
-        const int d = FP8 ? 32 * (st >> 1) + 16 * half + 8 * (st & 1) : 16 * st + 8 * half;
-        q[x][st] = *reinterpret_cast<const bf16x8*>(p + d);
-      }
-      if (a.tree_mask) {
-        lim[x] = max(seq.ctx, 0);
-        word[x] = a.tree_mask[qrow] & (~0ull >> (64 - seq.n));
-      } else {
-        lim[x] = max(seq.lo, seq.ctx + tok0 + tok + 1);
-        word[x] = 0;
-      }
+    for (int st = 0; st < C::STEPS; ++st) {
+      const int d = FP8 ? 32 * (st >> 1) + 16 * half + 8 * (st & 1) : 16 * st + 8 * half;
+      q[st] = *reinterpret_cast<const bf16x8*>(p + d);
+    }
+    if (a.tree_mask) {
+      lim = max(seq.ctx, 0);
+      word = a.tree_mask[qrow] & (~0ull >> (64 - seq.n));
+    } else {
+      lim = max(seq.lo, seq.ctx + tok0 + tok + 1);
+      word = 0;
     }
     take_ids(first_page, first_ids);
     // q is here before the key loop: a wait for it inside would wait for the tiles in flight too
     auto wait_q = [&]() {
 #pragma unroll
-      for (int x = 0; x < QT; ++x)
-#pragma unroll
-        for (int st = 0; st < C::STEPS; ++st) asm volatile("" ::"v"(__builtin_bit_cast(i32x4, q[x][st])));
+      for (int st = 0; st < C::STEPS; ++st) asm volatile("" ::"v"(__builtin_bit_cast(i32x4, q[st])));
     };
     // keys below this are seen by every row
     const int all_see = a.tree_mask ? max(seq.ctx, 0) : max(seq.lo, seq.ctx + tok0 + 1);
 
-    v16f o[QT][C::DT];
-    float m[QT], l[QT];
+    v16f o[C::DT];
+    float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int x = 0; x < QT; ++x) {
-      m[x] = -INFINITY;
-      l[x] = 0.f;
-#pragma unroll
-      for (int d = 0; d < C::DT; ++d) o[x][d] = v16f{};
-    }
+    for (int d = 0; d < C::DT; ++d) o[d] = v16f{};
 
     // -------- scores of one key tile. Each product's operand is read from LDS kAhead products
     // earlier, and the fences keep that order: left alone, the compiler reads right before use and every
     // product waits for its own read.
-    v16f sc[QT][C::KT];
+    v16f sc[C::KT];
     auto scores = [&](const uint8_t* kt_lds) {
 #pragma unroll
-      for (int x = 0; x < QT; ++x)
-#pragma unroll
-        for (int t = 0; t < C::KT; ++t) sc[x][t] = v16f{};
+      for (int t = 0; t < C::KT; ++t) sc[t] = v16f{};
       constexpr int kReads = C::KT * C::STEPS / (FP8 ? 2 : 1);   // 16 bytes: one step of bf16, two of e4m3
       constexpr int kAhead = FP8 ? 3 : 6;
       i32x4 raw[kReads];
@@ -446,15 +438,11 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bf16x8 k = bf16_of_e4m3(raw[i][2 * e], raw[i][2 * e + 1]);
-#pragma unroll
-            for (int x = 0; x < QT; ++x)
-              sc[x][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][2 * st + e], sc[x][t], 0, 0, 0);
+            sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[2 * st + e], sc[t], 0, 0, 0);
           }
         } else {
           const bf16x8 k = __builtin_bit_cast(bf16x8, raw[i]);
-#pragma unroll
-          for (int x = 0; x < QT; ++x)
-            sc[x][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][st], sc[x][t], 0, 0, 0);
+          sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[st], sc[t], 0, 0, 0);
         }
         fence_reads();
       }
@@ -462,89 +450,78 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
 
     // -------- the softmax step in four pieces: caps and masks, the rows' maxima, a moved maximum, and
     // the weights as the next product's operand
-    bf16x8 pb[QT][NK / 16];
-    f16x8 pf[QT][NK / 16];
+    bf16x8 pb[NK / 16], pl[NK / 16];
+    f16x8 pf[NK / 16];
     auto mask = [&](int key0) {
       if constexpr (CAP) {
-#pragma unroll
-        for (int x = 0; x < QT; ++x)
-#pragma unroll
-          for (int t = 0; t < C::KT; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              // cap tanh(y) = cap (1 - 2 / (e^2y + 1)), in units of log2 e
-              const float e = __builtin_amdgcn_exp2f(sc[x][t][i] * c);
-              sc[x][t][i] = cap2 - 2.f * cap2 * __builtin_amdgcn_rcpf(e + 1.f);
-            }
-      }
-      if (key0 + NK <= all_see && !careful) return;
-#pragma unroll
-      for (int x = 0; x < QT; ++x) {
-        // bit k: key0 + k is seen
-        const int n = lim[x] - key0;
-        uint64_t see = n >= 64 ? ~0ull : (n <= 0 ? 0ull : ~0ull >> (64 - n));
-        if (a.tree_mask) {
-          const int b = key0 - seq.ctx;   // the first key's bit
-          see |= b >= 64 || b <= -64 ? 0ull : (b >= 0 ? word[x] >> b : word[x] << -b);
-        }
-        if (careful) {
-#pragma unroll
-          for (int g = 0; g < NK / 16; ++g)
-            if (!group_ok(key0 + 16 * g)) see &= ~(0xFFFFull << (16 * g));
-        }
-        see >>= 4 * half;
-#pragma unroll
-        for (int t = 0; t < C::KT; ++t) {
-          const uint32_t bits = (uint32_t)(see >> (32 * t));
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            sc[x][t][i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? sc[x][t][i] : -INFINITY;
-        }
-      }
-    };
-    float mx[QT];
-    auto maxima = [&]() {
-#pragma unroll
-      for (int x = 0; x < QT; ++x) {
-        float v = sc[x][0][0];
-#pragma unroll
-        for (int t = 0; t < C::KT; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v = fmaxf(v, sc[x][t][i]);
-        v = swap_max(v);
-        mx[x] = (CAP ? v : v * c) - kBias;
-      }
-    };
-    auto move_max = [&]() {
-#pragma unroll
-      for (int x = 0; x < QT; ++x)
-        if (__any(mx[x] > m[x] + kMoveMax)) {
-          const float mn = fmaxf(m[x], mx[x]);
-          const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - mn);
-          m[x] = mn;
-          l[x] *= f;
-#pragma unroll
-          for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[x][d][i] *= f;
-        }
-    };
-    auto weights = [&](const v16f (&z)[QT][C::KT]) {
-#pragma unroll
-      for (int x = 0; x < QT; ++x) {
-        const float ms = m[x] == -INFINITY ? 0.f : m[x];
-        float sum = 0.f;
 #pragma unroll
         for (int t = 0; t < C::KT; ++t)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float p = __builtin_amdgcn_exp2f(CAP ? z[x][t][i] - ms : __builtin_fmaf(z[x][t][i], c, -ms));
-            sum += p;
-            if constexpr (FP8) pf[x][2 * t + i / 8][i % 8] = (_Float16)p;
-            else pb[x][2 * t + i / 8][i % 8] = (__bf16)p;
+            // cap tanh(y) = cap (1 - 2 / (e^2y + 1)), in units of log2 e
+            const float e = __builtin_amdgcn_exp2f(sc[t][i] * c);
+            sc[t][i] = cap2 - 2.f * cap2 * __builtin_amdgcn_rcpf(e + 1.f);
           }
-        l[x] += sum;
       }
+      if (key0 + NK <= all_see && !careful) return;
+      // bit k: key0 + k is seen
+      const int n = lim - key0;
+      uint64_t see = n >= 64 ? ~0ull : (n <= 0 ? 0ull : ~0ull >> (64 - n));
+      if (a.tree_mask) {
+        const int b = key0 - seq.ctx;   // the first key's bit
+        see |= b >= 64 || b <= -64 ? 0ull : (b >= 0 ? word >> b : word << -b);
+      }
+      if (careful) {
+#pragma unroll
+        for (int g = 0; g < NK / 16; ++g)
+          if (!group_ok(key0 + 16 * g)) see &= ~(0xFFFFull << (16 * g));
+      }
+      see >>= 4 * half;
+#pragma unroll
+      for (int t = 0; t < C::KT; ++t) {
+        const uint32_t bits = (uint32_t)(see >> (32 * t));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[t][i] = (bits >> (8 * (i / 4) + i % 4)) & 1 ? sc[t][i] : -INFINITY;
+      }
+    };
+    float mx;   // the row's largest score of the tile, in units of log2 e
+    auto maxima = [&]() {
+      float v = sc[0][0];
+#pragma unroll
+      for (int t = 0; t < C::KT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v = fmaxf(v, sc[t][i]);
+      v = swap_max(v);
+      mx = (CAP ? v : v * c) - kBias;
+    };
+    auto move_max = [&]() {
+      if (!__any(mx > m + kMoveMax)) return;
+      const float mn = fmaxf(m, mx);
+      const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= f;
+    };
+    auto weights = [&]() {
+      const float ms = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < C::KT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p = __builtin_amdgcn_exp2f(CAP ? sc[t][i] - ms : __builtin_fmaf(sc[t][i], c, -ms));
+          sum += p;
+          if constexpr (FP8) {
+            pf[2 * t + i / 8][i % 8] = (_Float16)p;
+          } else {
+            pb[2 * t + i / 8][i % 8] = (__bf16)p;
+            if constexpr (C::kSplit) pl[2 * t + i / 8][i % 8] = (__bf16)(p - (float)(__bf16)p);
+          }
+        }
+      l += sum;
     };
 
     auto values = [&](const uint8_t* v) {
@@ -574,15 +551,12 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
         if (i + kAhead < kReads) read(i + kAhead);
         fence_reads();
         const int st = i / C::DT, d = i % C::DT;
-#pragma unroll
-        for (int x = 0; x < QT; ++x) {
-          if constexpr (FP8)
-            o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f16_of_e4m3(raw[i][0], raw[i][1]), pf[x][st], o[x][d],
-                                                             0, 0, 0);
-          else
-            o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, raw[i]), pb[x][st],
-                                                              o[x][d], 0, 0, 0);
-        }
+        const bf16x8 vb = __builtin_bit_cast(bf16x8, raw[i]);
+        if constexpr (FP8)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f16_of_e4m3(raw[i][0], raw[i][1]), pf[st], o[d], 0, 0, 0);
+        else
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, pb[st], o[d], 0, 0, 0);
+        if constexpr (C::kSplit) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, pl[st], o[d], 0, 0, 0);
         fence_reads();
       }
     };
@@ -615,7 +589,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
         mask(t * NK);
         maxima();
         move_max();
-        weights(sc);
+        weights();
         if (left == 0) wait_vm<0>();
         else if (left == 1) wait_vm<2 * L>();
         else wait_vm<3 * L>();
@@ -656,7 +630,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
         mask(t * NK);
         maxima();
         move_max();
-        weights(sc);
+        weights();
         __builtin_amdgcn_s_setprio(1);
         values(st + C::TILE);
         __builtin_amdgcn_s_setprio(0);
@@ -668,56 +642,49 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     const bool complete = begins && ends;
     float* const slot = partials + (size_t)(2 * w + (begins ? 1 : 0)) * C::SLOT;
     if constexpr (KW == 1) {
+      const int r = rw * 32 + col;
+      const float sum = swap_sum(l);
+      if (r < rows) {
+        if (complete) {
+          const int tok = r / a.G, head = h * a.G + r - tok * a.G;
+          const size_t at = (size_t)(row0 + tok) * a.Hq + head;
+          const float f = sum > 0.f ? vs / sum : 0.f;
 #pragma unroll
-      for (int x = 0; x < QT; ++x) {
-        const int r = (rw * QT + x) * 32 + col;
-        const float sum = swap_sum(l[x]);
-        if (r < rows) {
-          if (complete) {
-            const int tok = r / a.G, head = h * a.G + r - tok * a.G;
-            const size_t at = (size_t)(row0 + tok) * a.Hq + head;
-            const float f = sum > 0.f ? vs / sum : 0.f;
+          for (int d = 0; d < C::DT; ++d)
 #pragma unroll
-            for (int d = 0; d < C::DT; ++d)
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint2*>(a.out + at * D + 32 * d + 8 * i + 4 * half) =
+                  make_uint2(pack_bf16x2(o[d][4 * i] * f, o[d][4 * i + 1] * f),
+                             pack_bf16x2(o[d][4 * i + 2] * f, o[d][4 * i + 3] * f));
+          if (a.lse && half == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+        } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint2*>(a.out + at * D + 32 * d + 8 * i + 4 * half) =
-                    make_uint2(pack_bf16x2(o[x][d][4 * i] * f, o[x][d][4 * i + 1] * f),
-                               pack_bf16x2(o[x][d][4 * i + 2] * f, o[x][d][4 * i + 3] * f));
-            if (a.lse && half == 0) a.lse[at] = sum > 0.f ? (m[x] + log2f(sum)) * kLn2 : -INFINITY;
-          } else {
+          for (int d = 0; d < C::DT; ++d)
 #pragma unroll
-            for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(slot + (size_t)r * D + 32 * d + 8 * i + 4 * half) =
-                    make_float4(o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]);
-            if (half == 0) {
-              slot[C::M * D + r] = m[x];
-              slot[C::M * D + C::M + r] = sum;
-            }
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(slot + (size_t)r * D + 32 * d + 8 * i + 4 * half) =
+                  make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
+          if (half == 0) {
+            slot[C::M * D + r] = m;
+            slot[C::M * D + C::M + r] = sum;
           }
         }
       }
     } else {
       // every wave's O, [row][D] float32 with chunks swapped by row, in its own stages
-#pragma unroll
-      for (int x = 0; x < QT; ++x) {
-        const int r = x * 32 + col;
-        const float sum = swap_sum(l[x]);
-        if (half == 0) {
-          row_m[kw][r] = m[x];
-          row_l[kw][r] = sum;
-        }
-#pragma unroll
-        for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int chunk = (8 * d + 2 * i + half) ^ (r & 15);
-            *reinterpret_cast<float4*>(stages + r * D * 4 + chunk * 16) =
-                make_float4(o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]);
-          }
+      const float sum = swap_sum(l);
+      if (half == 0) {
+        row_m[kw][col] = m;
+        row_l[kw][col] = sum;
       }
+#pragma unroll
+      for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int chunk = (8 * d + 2 * i + half) ^ (col & 15);
+          *reinterpret_cast<float4*>(stages + col * D * 4 + chunk * 16) =
+              make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
+        }
       __syncthreads();
       for (int i = tid; i < rows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c4 = i % (D / 4);
@@ -879,31 +846,31 @@ constexpr int parts_of(int M, int D) { return M == 128 && D < 256 ? 512 : 256; }
 // From this many segments on, one workgroup takes a whole one
 constexpr long kWholeSegments = 1536;
 
-// Rows of a workgroup's tile for calls of at most max_q tokens per sequence
-static int tile_rows(int max_q, int G, int D) {
-  const long rows = (long)max_q * G;
-  return rows <= 32 ? 32 : (rows <= 64 && D < 256 ? 64 : 128);
-}
+// Rows of a workgroup's tile for calls of at most max_q tokens per sequence: 32 with a wave's own
+// keys where they hold a sequence's whole query group, else 128 sharing them (60 rows of 5 tokens,
+// 64 sequences of up to 8192: 44 us; two 32-row tiles per wave of own keys: 53).
+static int tile_rows(int max_q, int G) { return (long)max_q * G <= 32 ? 32 : 128; }
 static size_t slot_floats(int M, int D) { return (size_t)M * D + 2 * M; }
 
 size_t attention_workspace_bytes(int S, int max_q, int Hq, int Hkv, int D) {
   (void)S;
-  const int M = tile_rows(max_q, Hq / Hkv, D);
+  const int M = tile_rows(max_q, Hq / Hkv);
   return parts_of(M, D) * 2 * (slot_floats(M, D) * 4 + sizeof(PartDesc));
 }
 
-template <int D, bool FP8, int QT, int RW, int KW, int NK, bool CAP>
+template <int D, bool FP8, int RW, int KW, int NK, bool CAP>
 static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
-  using C = Attn<D, FP8, QT, RW, KW, NK, CAP>;
-  auto* kernel = attention_kernel<D, FP8, QT, RW, KW, NK, CAP>;
+  using C = Attn<D, FP8, RW, KW, NK, CAP>;
+  auto* kernel = attention_kernel<D, FP8, RW, KW, NK, CAP>;
   constexpr int kParts = parts_of(C::M, D);
   float* partials = static_cast<float*>(a.ws);
   PartDesc* descs = reinterpret_cast<PartDesc*>(partials + 2 * kParts * slot_floats(C::M, D));
   const int TB = C::M / a.G;
   // at least this many segments, by the rows of q alone (a device-side count would come too late)
   const long segments = (long)a.Hkv * (a.T / TB);
-  if (KW == 1 && segments >= kWholeSegments) {
-    const int grid = (int)((long)a.Hkv * ((a.T + TB - 1) / TB + a.S));
+  const long bound = (long)a.Hkv * ((a.T + TB - 1) / TB + a.S);
+  if (KW == 1 && segments >= kWholeSegments && bound <= min(4 * segments, 1l << 22)) {
+    const int grid = (int)bound;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, true, 0, partials,
                        descs);
     return hipGetLastError();
@@ -926,12 +893,8 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
 template <int D, bool FP8, bool CAP>
 static hipError_t launch_rows(const AttnArgs& a, hipStream_t stream) {
   constexpr int NKs = FP8 || D == 64 ? (D == 256 ? 32 : 64) : 32;
-  const int M = tile_rows(a.max_q, a.G, D);
-  if (M == 32) return launch_one<D, FP8, 1, 1, D == 256 ? 2 : 4, NKs, CAP>(a, stream);
-  if constexpr (D < 256) {
-    if (M == 64) return launch_one<D, FP8, 2, 1, 4, D == 64 && FP8 ? 64 : NKs, CAP>(a, stream);
-  }
-  return launch_one<D, FP8, 1, 4, 1, D == 256 ? 32 : 64, CAP>(a, stream);
+  if (tile_rows(a.max_q, a.G) == 32) return launch_one<D, FP8, 1, D == 256 ? 2 : 4, NKs, CAP>(a, stream);
+  return launch_one<D, FP8, 4, 1, D == 256 ? 32 : 64, CAP>(a, stream);
 }
 
 template <int D>

@@ -191,6 +191,62 @@ def test_prefill(ns, kvs, Hq, Hkv, D, page, prefixes, cap, fp8):
     run_check(c, "prefill", None if prefixes is None else np.array(prefixes, np.int32), sees, cap=cap)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_row_tiles(fp8):
+    """Over 1536 row tiles: a workgroup takes a whole one, nothing is split or joined."""
+    ns, kvs, pre = [1300, 0, 5, 870], [1400, 3, 5, 870], [200, 0, 0, 870]
+    c = make_case(ns, kvs, 96, 8, 64, 32, fp8, seed=12, lead=3, tail=1)
+    assert 8 * (c.T // (128 // 12)) >= 1536
+    run_check(c, "prefill", np.array(pre, np.int32), [oracle.visible_prefill(n, k, p) for n, k, p in zip(ns, kvs, pre)])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_what_the_workspace_held_does_not_matter(fp8):
+    """Few and many sequences (one description per segment, or per part), each with the workspace full of other bytes."""
+    for which, ns, kvs in (("tree", [1] * 6, [1, 700, 3, 40, 5000, 17]), ("tree", [1] * 600, [1 + i % 90 for i in range(600)]),
+                           ("prefill", [100, 3], [150, 900])):
+        c = make_case(ns, kvs, 4, 1, 128, 16, fp8, seed=3)
+        d = Dev(c)
+        sees = [oracle.visible_tree(n, k, None) if which == "tree" else oracle.visible_prefill(n, k, 0) for n, k in zip(ns, kvs)]
+        for byte in (0x01, 0x7F, 0xFF, 0x00):
+            d.ws.fill_(byte)
+            d.out.fill_(0x7FC1)
+            d.lse.fill_(7.0)
+            d.call(which)
+            torch.cuda.synchronize()
+            check(c, bits_of(d.out), d.lse.cpu().numpy(), sees, c.D ** -0.5, 0.0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_far_pages(fp8):
+    """Pages whose byte offsets pass 2^32 (and element offsets 2^31): the last pages of a large pool, strided."""
+    Hkv, D, page = 8, 128, 64
+    stride = 4 * Hkv * page * D        # elements: half of every page's stretch belongs to nothing
+    pages = (1 << 32) // stride + 20
+    es = 1 if fp8 else 2
+    pool = torch.empty(pages * stride * es, dtype=torch.uint8, device=DEV)
+    pool.view(torch.int32).fill_(0x7FC07FC0 if not fp8 else 0x7F7F7F7F)
+    kvs = [500, 70]
+    c = make_case([1, 40], kvs, 16, Hkv, D, page, fp8, seed=5)
+    far = np.array([pages - 1 - 3 * i for i in range(c.kv.shape[0])], np.int32)
+    view = pool.view(torch.uint8 if fp8 else torch.int16).view(pages, stride)
+    for i, p in enumerate(far):
+        view[int(p), :2 * Hkv * page * D] = up(c.kv[i] if fp8 else c.kv[i].view(np.int16)).reshape(-1)
+    for s, k in enumerate(kvs):
+        n = -(-k // page)
+        c.table[s, :n] = far[c.table[s, :n]]
+    d = Dev(c)
+    d.out.fill_(0x7FC1)
+    d.lse.fill_(7.0)
+    note(f"far pages fp8={fp8} pages={pages} stride={stride}")
+    L.moe_tree_attention(d.q, c.q.shape[1], pool.data_ptr(), pool.data_ptr() + Hkv * page * D * es,
+                         L.KV_E4M3 if fp8 else L.KV_BF16, d.ks if fp8 else None, d.vs if fp8 else None, pages, page, stride,
+                         up(c.table), c.table.shape[1], d.cu, d.kvl, None, 2, c.T, 40, c.Hq, Hkv, D, D ** -0.5, 0.0, d.out,
+                         d.lse, d.ws, d.ws_bytes)
+    torch.cuda.synchronize()
+    check(c, bits_of(d.out), d.lse.cpu().numpy(), [oracle.visible_tree(n, k, None) for n, k in zip(c.ns, kvs)], D ** -0.5, 0.0)
+
+
 @pytest.mark.parametrize("which", ["tree", "prefill"])
 def test_fewer_cached_tokens_than_queries(which):
     """kv_lens below the query count: the first rows lie before the cache and see nothing."""
