@@ -47,7 +47,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kMoveMax = 8.0f;    // a running maximum moves when a score exceeds it by this (base 2)
-constexpr int kSegCost = 64;        // a segment's fixed cost, in keys, for the work split
 
 // 16-byte chunk swap of key k's row (CPR chunks of it), for LDS's 64 banks of 4 bytes: 16 consecutive
 // keys' same chunk (a step of K's reads) and the 64 or 32 bytes of {4h..4h+3} (8-bit: and 8+4h..) of a
@@ -116,12 +115,12 @@ __device__ __forceinline__ f16x8 f16_of_e4m3(int a, int b) {
 struct SeqTiles {
   int row0, n, kv, ctx, lo, MT;
   __device__ __forceinline__ int vis(int i, int TB) const { return max(lo, ctx + min(n, (i + 1) * TB)); }
-  // cost of tiles 0..mt-1 of one head: vis + kSegCost each, in closed form; 1 each where segments are
-  // taken whole
-  __device__ __forceinline__ long cost(int mt, int TB, bool whole) const {
-    if (whole) return mt;
+  // cost of tiles 0..mt-1 of one head: vis + fixed each, in closed form (fixed: what a segment costs
+  // besides its keys, in keys); 1 each where segments are taken whole (fixed < 0)
+  __device__ __forceinline__ long cost(int mt, int TB, int fixed) const {
+    if (fixed < 0) return mt;
     const long star = lo > ctx ? min(MT, (lo - ctx) / TB) : 0;   // the tiles with ctx + (i + 1) TB <= lo
-    long f = (long)mt * kSegCost + min((long)mt, star) * lo;
+    long f = (long)mt * fixed + min((long)mt, star) * lo;
     if (mt > star) {
       f += (mt - star) * ctx + (long)TB * (((long)mt * (mt + 1) - star * (star + 1)) / 2);
       if (mt == MT) f -= (long)ctx + (long)MT * TB - max(lo, ctx + n);
@@ -190,6 +189,9 @@ struct Attn {
   // free (decode of 64 sequences takes as long, its error is 0.0017 of the output instead of 0.0023, that of the
   // output's own rounding). Tiles of more rows round them once (5 drafted tokens of 12 heads: 53 us, split 57).
   static constexpr bool kSplit = !FP8 && RW == 1;
+  // What a segment costs besides its keys, in keys (its q, its first tile's latency, its result: about
+  // 5 us, a tile of 64 keys 1.2 to 1.7)
+  static constexpr int kSegCost = RW == 1 ? 128 : 192;
   static constexpr int kMinPart = RW == 1 ? KW * NK : 4 * NK;   // a part's cost in keys is at least this
   static constexpr int SLOT = M * D + 2 * M;    // floats of a partial: O [M][D], then m and l per row
   static_assert(NX % RW == 0 && RPI <= 16 && NK <= 64, "tile shape");
@@ -212,13 +214,14 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int rw = wave % RW, kw = wave / RW;
   const int half = lane >> 5, col = lane & 31;
+  const int fixed = whole ? -1 : C::kSegCost;
   // -------- which part of the line of segments is this workgroup's
   const int per = (a.S + kThreads - 1) / kThreads;
   const int s_lo = min(tid * per, a.S), s_hi = min(s_lo + per, a.S);
   long mine = 0;
   for (int s = s_lo; s < s_hi; ++s) {
     const SeqTiles t = seq_tiles(a, s, TB);
-    mine += t.cost(t.MT, TB, whole) * a.Hkv;
+    mine += t.cost(t.MT, TB, fixed) * a.Hkv;
   }
   long incl = mine;
 #pragma unroll
@@ -252,7 +255,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     long r = u - before;
     for (int s = s_lo; s < s_hi; ++s) {
       const SeqTiles t = seq_tiles(a, s, TB);
-      const long c = t.cost(t.MT, TB, whole) * a.Hkv;
+      const long c = t.cost(t.MT, TB, fixed) * a.Hkv;
       if (r < c) {
         found_s = s;
         found_seq = t;
@@ -268,18 +271,18 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   SeqTiles seq = uniform(found_seq);
   int h, mt;
   {
-    const long per_head = seq.cost(seq.MT, TB, whole);
+    const long per_head = seq.cost(seq.MT, TB, fixed);
     h = uni((int)div_pos(rem, per_head));
     rem -= h * per_head;
     int lo = 0, hi = seq.MT;   // the largest tile with cost(tile) <= rem, 64 candidates at a time
     while (hi - lo > 1) {
       const int step = (hi - lo + 63) >> 6, at = lo + lane * step;
-      const int n = __popcll(__ballot(at < hi && seq.cost(at, TB, whole) <= rem));
+      const int n = __popcll(__ballot(at < hi && seq.cost(at, TB, fixed) <= rem));
       lo = uni(lo + (n - 1) * step);
       hi = uni(min(hi, lo + step));
     }
     mt = lo;
-    rem -= seq.cost(mt, TB, whole);
+    rem -= seq.cost(mt, TB, fixed);
   }
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)sm;
@@ -309,12 +312,18 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   while (u < u_end) {
     // -------- the segment: rows, keys, and this part's share of its tiles
     const int vis = seq.vis(mt, TB);
-    const long seg_cost = whole ? 1 : vis + kSegCost;
+    const long seg_cost = whole ? 1 : vis + C::kSegCost;
     const long seg_end = u - rem + seg_cost;
-    const bool begins = rem == 0, ends = seg_end <= u_end;
+    const bool ends = seg_end <= u_end;
     const int ntiles = (vis + NK - 1) / NK;
-    const int t0 = min(ntiles, (int)(rem / NK));
-    const int t1 = ends ? ntiles : min(ntiles, (int)((rem + u_end - u) / NK));
+    // A segment's tiles in proportion to the share of its cost: the part after a border starts where
+    // the part before it stops. A part whose share of the front is no tile leaves the segment to the
+    // next one, which then begins it; no tile at all (nothing is seen) belongs to its first unit.
+    const int t0 = uni((int)div_pos(rem * ntiles, seg_cost));
+    const int t1 = ends ? ntiles : uni((int)div_pos((rem + u_end - u) * ntiles, seg_cost));
+    const bool begins = ntiles > 0 ? t0 == 0 : rem == 0;
+    const bool mine_too = ntiles > 0 ? t1 > 0 : begins;
+    if (mine_too) {
     const int tok0 = mt * TB, rows = min(TB, seq.n - tok0) * a.G;
     const int row0 = seq.row0 + tok0;
     const float ks = FP8 ? a.k_scale[h] : 1.f, vs = FP8 ? a.v_scale[h] : 1.f;
@@ -639,7 +648,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     }
 
     // -------- the segment's result, or this part's partial
-    const bool complete = begins && ends;
+    const bool complete = begins && (ends || ntiles == 0);
     float* const slot = partials + (size_t)(2 * w + (begins ? 1 : 0)) * C::SLOT;
     if constexpr (KW == 1) {
       const int r = rw * 32 + col;
@@ -719,9 +728,10 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     if (begins && tid == 0 && !whole) {
       if (desc_tiles > 0)
         descs[((size_t)s * a.Hkv + h) * desc_tiles + mt] =
-            PartDesc{row0, ends ? 0 : rows, h, w, ends ? w : split.of(seg_end - 1)};
-      else if (!ends)
+            PartDesc{row0, complete ? 0 : rows, h, w, complete ? w : split.of(seg_end - 1)};
+      else if (!complete)
         descs[w] = PartDesc{row0, rows, h, w, split.of(seg_end - 1)};
+    }
     }
 
     // -------- the next segment
