@@ -853,8 +853,16 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 // the register file and LDS hold two (128-row tiles of head_dim 64 and 128)
 constexpr int parts_of(int M, int D) { return M == 128 && D < 256 ? 512 : 256; }
 
-// From this many segments on, one workgroup takes a whole one
-constexpr long kWholeSegments = 1536;
+// Whether a workgroup takes a whole segment (no partials, no join) rather than an equal part of the
+// line: `segments` as the rows of q say, `keys` as the block table allows at most. Whole and split
+// measured, shared tiles: 1639 segments of one 16384-token prompt 868 and 1007 us; about 500 of up to
+// 1024 keys 37 and 54; 100 of up to 250 keys 15 and 22; 409 of up to 4096 keys 98 and 92. A wave's own
+// keys: 256 sequences of up to 1000 keys 21 and 30; 3 of up to 200 13 and 15; one of 777 19 and 15.
+static bool take_whole(bool shared_tiles, long segments, long keys) {
+  if (keys <= 512) return true;
+  if (!shared_tiles) return segments >= 128 && keys <= 1024;
+  return segments >= 1536 || (segments >= 256 && keys <= 2048);
+}
 
 // Rows of a workgroup's tile for calls of at most max_q tokens per sequence: 32 with a wave's own
 // keys where they hold a sequence's whole query group, else 128 sharing them (60 rows of 5 tokens,
@@ -876,10 +884,11 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   float* partials = static_cast<float*>(a.ws);
   PartDesc* descs = reinterpret_cast<PartDesc*>(partials + 2 * kParts * slot_floats(C::M, D));
   const int TB = C::M / a.G;
-  // at least this many segments, by the rows of q alone (a device-side count would come too late)
-  const long segments = (long)a.Hkv * (a.T / TB);
+  // segments by the rows of q alone (a device-side count would come too late); one per sequence where a
+  // tile holds its whole query group
+  const long segments = (long)a.Hkv * (KW == 1 ? a.T / TB : min(a.S, a.T));
   const long bound = (long)a.Hkv * ((a.T + TB - 1) / TB + a.S);
-  if (KW == 1 && segments >= kWholeSegments && bound <= min(4 * segments, 1l << 22)) {
+  if (take_whole(KW == 1, segments, (long)a.max_pages << a.page_shift) && bound <= 1l << 22) {
     const int grid = (int)bound;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, true, 0, partials,
                        descs);

@@ -87,7 +87,13 @@ def check(c, out_bits, lse, sees, scale, cap, guard=0x7FC1):
     return worst
 
 
-def run_check(c, which, extra_np, sees, scale=None, cap=0.0, lse=True, tag=""):
+def run_check(c, which, extra_np, sees, scale=None, cap=0.0, lse=True, tag="", wide=False):
+    """wide: a block table of far more columns than the sequences use (what they may hold, not what they do, decides
+    how the kernels split the keys)."""
+    if wide:
+        t = np.full((c.table.shape[0], 131072 // c.page), 1 << 30, np.int32)
+        t[:, :c.table.shape[1]] = c.table
+        c.table = t
     d = Dev(c)
     d.out.fill_(0x7FC1)
     d.lse.fill_(7.0)
@@ -105,13 +111,14 @@ HEADS = [(12, 1, 128), (96, 8, 128), (8, 2, 64), (7, 1, 64), (1, 1, 128), (4, 4,
          (32, 1, 128), (128, 1, 64), (40, 1, 128)]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("Hq,Hkv,D", HEADS)
-def test_single_tokens(Hq, Hkv, D, fp8):
+def test_single_tokens(Hq, Hkv, D, fp8, wide):
     """One token per sequence, lengths around the tile and page borders."""
     kvs = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1000]
     c = make_case([1] * len(kvs), kvs, Hq, Hkv, D, 16, fp8, seed=Hq + D)
-    run_check(c, "tree", None, [oracle.visible_tree(1, k, None) for k in kvs])
+    run_check(c, "tree", None, [oracle.visible_tree(1, k, None) for k in kvs], wide=wide)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -142,8 +149,9 @@ def test_tree_sizes(n, fp8):
     run_check(c, "tree", np.concatenate(w).view(np.int64), [oracle.visible_tree(n, k, x) for k, x in zip(kvs, w)])
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_empty_rows(fp8):
+def test_empty_rows(fp8, wide):
     """Words that leave a row nothing, with and without a context; bits past the sequence's own tokens change nothing."""
     ns, kvs = [4, 3, 2, 1], [4, 3, 40, 1]
     c = make_case(ns, kvs, 12, 1, 128, 16, fp8, seed=1)
@@ -152,7 +160,7 @@ def test_empty_rows(fp8):
     for n, k in zip(ns, kvs):
         sees.append(oracle.visible_tree(n, k, words[at:at + n]))
         at += n
-    run_check(c, "tree", words.view(np.int64), sees)
+    run_check(c, "tree", words.view(np.int64), sees, wide=wide)
 
 
 @pytest.mark.parametrize("cap", [0.0, 4.0])
@@ -182,13 +190,14 @@ PREFILL = [
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("ns,kvs,Hq,Hkv,D,page,prefixes,cap", PREFILL)
-def test_prefill(ns, kvs, Hq, Hkv, D, page, prefixes, cap, fp8):
+def test_prefill(ns, kvs, Hq, Hkv, D, page, prefixes, cap, fp8, wide):
     c = make_case(ns, kvs, Hq, Hkv, D, page, fp8, seed=sum(ns) + D, lead=1, tail=2, q_extra=16)
     pre = prefixes or [0] * len(ns)
     sees = [oracle.visible_prefill(n, k, p) for n, k, p in zip(ns, kvs, pre)]
-    run_check(c, "prefill", None if prefixes is None else np.array(prefixes, np.int32), sees, cap=cap)
+    run_check(c, "prefill", None if prefixes is None else np.array(prefixes, np.int32), sees, cap=cap, wide=wide)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -203,9 +212,10 @@ def test_many_row_tiles(fp8):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_what_the_workspace_held_does_not_matter(fp8):
     """Few and many sequences (one description per segment, or per part), each with the workspace full of other bytes."""
-    for which, ns, kvs in (("tree", [1] * 6, [1, 700, 3, 40, 5000, 17]), ("tree", [1] * 600, [1 + i % 90 for i in range(600)]),
+    for which, ns, kvs in (("tree", [1] * 6, [1, 700, 3, 40, 5000, 17]), ("tree", [1] * 600, [1 + i % 90 + 600 * (i == 5) for i in range(600)]),
                            ("prefill", [100, 3], [150, 900])):
         c = make_case(ns, kvs, 4, 1, 128, 16, fp8, seed=3)
+        c.table = np.concatenate([c.table, np.full((len(ns), 4096), -7, np.int32)], 1)
         d = Dev(c)
         sees = [oracle.visible_tree(n, k, None) if which == "tree" else oracle.visible_prefill(n, k, 0) for n, k in zip(ns, kvs)]
         for byte in (0x01, 0x7F, 0xFF, 0x00):
@@ -247,26 +257,28 @@ def test_far_pages(fp8):
     check(c, bits_of(d.out), d.lse.cpu().numpy(), [oracle.visible_tree(n, k, None) for n, k in zip(c.ns, kvs)], D ** -0.5, 0.0)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("which", ["tree", "prefill"])
-def test_fewer_cached_tokens_than_queries(which):
+def test_fewer_cached_tokens_than_queries(which, wide):
     """kv_lens below the query count: the first rows lie before the cache and see nothing."""
     ns, kvs = [6, 5, 70 if which == "prefill" else 50], [4, 0, 33]
     c = make_case(ns, kvs, 12, 1, 128, 16, False, seed=2)
     sees = []
     for n, k in zip(ns, kvs):
         sees.append(oracle.visible_tree(n, k, None) if which == "tree" else oracle.visible_prefill(n, k, 0))
-    run_check(c, which, None, sees)
+    run_check(c, which, None, sees, wide=wide)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("n", [1, 30])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_pages_outside_the_pool_are_unseen(fp8, n):
+def test_pages_outside_the_pool_are_unseen(fp8, n, wide):
     c = make_case([n, n], [200, 90], 12, 1, 128, 16, fp8, seed=3)
     c.table[0, 2], c.table[0, 7], c.table[1, 0] = -1, c.kv.shape[0], 2 ** 31 - 1
     see = [oracle.visible_tree(n, k, None) for k in c.kvs]
     see[0][:, 32:48] = see[0][:, 112:128] = False
     see[1][:, :16] = False
-    run_check(c, "tree", None, see)
+    run_check(c, "tree", None, see, wide=wide)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -277,11 +289,12 @@ def test_long_cache(fp8):
     run_check(c, "tree", None, [oracle.visible_tree(1, k, None) for k in kvs])
 
 
-def test_many_sequences():
+@pytest.mark.parametrize("wide", [False, True])
+def test_many_sequences(wide):
     rng = np.random.default_rng(0)
     kvs = [int(x) for x in rng.integers(1, 60, 700)]
     c = make_case([1] * 700, kvs, 4, 2, 64, 16, False, seed=6)
-    run_check(c, "tree", None, [oracle.visible_tree(1, k, None) for k in kvs])
+    run_check(c, "tree", None, [oracle.visible_tree(1, k, None) for k in kvs], wide=wide)
 
 
 def test_same_bits_every_time():
