@@ -191,7 +191,7 @@ struct Attn {
   static constexpr bool kSplit = !FP8 && RW == 1;
   // What a segment costs besides its keys, in keys (its q, its first tile's latency, its result: about
   // 5 us, a tile of 64 keys 1.2 to 1.7)
-  static constexpr int kSegCost = RW == 1 ? 128 : 192;
+  static constexpr int kSegCost = RW == 1 ? 192 : 256;
   static constexpr int kMinPart = RW == 1 ? KW * NK : 4 * NK;   // a part's cost in keys is at least this
   static constexpr int SLOT = M * D + 2 * M;    // floats of a partial: O [M][D], then m and l per row
   static_assert(NX % RW == 0 && RPI <= 16 && NK <= 64, "tile shape");
@@ -316,11 +316,12 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     const long seg_end = u - rem + seg_cost;
     const bool ends = seg_end <= u_end;
     const int ntiles = (vis + NK - 1) / NK;
-    // A segment's tiles in proportion to the share of its cost: the part after a border starts where
-    // the part before it stops. A part whose share of the front is no tile leaves the segment to the
-    // next one, which then begins it; no tile at all (nothing is seen) belongs to its first unit.
-    const int t0 = uni((int)div_pos(rem * ntiles, seg_cost));
-    const int t1 = ends ? ntiles : uni((int)div_pos((rem + u_end - u) * ntiles, seg_cost));
+    // The fixed cost comes first: the part in which a segment begins takes that much fewer keys. The part
+    // after a border starts where the part before it stops. A part whose share of the front is no tile
+    // leaves the segment to the next one, which then begins it; no tile at all (nothing is seen) belongs
+    // to its first unit.
+    const int t0 = (int)(max(rem - C::kSegCost, 0l) / NK);
+    const int t1 = ends ? ntiles : (int)(max(rem + u_end - u - C::kSegCost, 0l) / NK);
     const bool begins = ntiles > 0 ? t0 == 0 : rem == 0;
     const bool mine_too = ntiles > 0 ? t1 > 0 : begins;
     if (mine_too) {
