@@ -75,6 +75,12 @@ __device__ __forceinline__ long uni(long v) {
   return (long)(((uint64_t)hi << 32) | lo);
 }
 
+__device__ __forceinline__ long read_lane(long v, int at) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, at);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), at);
+  return (long)(((uint64_t)hi << 32) | lo);
+}
+
 // 16 bytes per lane from base + voff to LDS address `lds` + 16 * lane. In asm, because the
 // compiler would wait for every such load in flight before any later LDS read; wait_vm counts them.
 // kOnce: the bytes are read by this wave alone and passed through the caches as such (decode of 24
@@ -216,12 +222,16 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   const int half = lane >> 5, col = lane & 31;
   const int fixed = whole ? -1 : C::kSegCost;
   // -------- which part of the line of segments is this workgroup's
-  const int per = (a.S + kThreads - 1) / kThreads;
-  const int s_lo = min(tid * per, a.S), s_hi = min(s_lo + per, a.S);
+  // Up to 64 sequences: one per lane, in every wave by itself. More: a stretch of them per thread, and
+  // two barriers.
+  const bool few = a.S <= 64;
+  const int per = few ? 1 : (a.S + kThreads - 1) / kThreads, place = few ? lane : tid;
+  const int s_lo = min(place * per, a.S), s_hi = min(s_lo + per, a.S);
   long mine = 0;
+  SeqTiles own{};
   for (int s = s_lo; s < s_hi; ++s) {
-    const SeqTiles t = seq_tiles(a, s, TB);
-    mine += t.cost(t.MT, TB, fixed) * a.Hkv;
+    own = seq_tiles(a, s, TB);
+    mine += own.cost(own.MT, TB, fixed) * a.Hkv;
   }
   long incl = mine;
 #pragma unroll
@@ -229,15 +239,18 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     const long o = __shfl_up(incl, d, 64);
     if (lane >= d) incl += o;
   }
-  if (lane == 63) scan_sum[wave] = incl;
-  __syncthreads();
-  long total = 0, before = incl - mine;
+  long total = read_lane(incl, 63), before = incl - mine;
+  if (!few) {
+    if (lane == 0) scan_sum[wave] = total;
+    __syncthreads();
+    total = 0;
 #pragma unroll
-  for (int i = 0; i < C::kWaves; ++i) {
-    if (i < wave) before += scan_sum[i];
-    total += scan_sum[i];
+    for (int i = 0; i < C::kWaves; ++i) {
+      if (i < wave) before += scan_sum[i];
+      total += scan_sum[i];
+    }
+    total = uni(total);
   }
-  total = uni(total);
   const int parts = (int)min((long)parts_max, whole ? total : (total + C::kMinPart - 1) / C::kMinPart);
   // Split: consecutive parts on one XCD (they walk neighbouring keys), however many there are on all
   // XCDs alike. Whole: the last tiles of a sequence, which see the most keys, first.
@@ -251,24 +264,39 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
   const Parts split(total, parts);
   long u = split.begin(w);
   const long u_end = split.begin(w + 1);
-  if (mine > 0 && u >= before && u < before + mine) {
-    long r = u - before;
-    for (int s = s_lo; s < s_hi; ++s) {
-      const SeqTiles t = seq_tiles(a, s, TB);
-      const long c = t.cost(t.MT, TB, fixed) * a.Hkv;
-      if (r < c) {
-        found_s = s;
-        found_seq = t;
-        found_rem = r;
-        break;
+  const bool here = mine > 0 && u >= before && u < before + mine;   // one place alone
+  int s;
+  long rem;
+  SeqTiles seq;
+  if (few) {
+    s = __ffsll((unsigned long long)__ballot(here)) - 1;
+    rem = u - read_lane(before, s);
+    seq.row0 = __builtin_amdgcn_readlane(own.row0, s);
+    seq.n = __builtin_amdgcn_readlane(own.n, s);
+    seq.kv = __builtin_amdgcn_readlane(own.kv, s);
+    seq.ctx = __builtin_amdgcn_readlane(own.ctx, s);
+    seq.lo = __builtin_amdgcn_readlane(own.lo, s);
+    seq.MT = __builtin_amdgcn_readlane(own.MT, s);
+  } else {
+    if (here) {
+      long r = u - before;
+      for (int i = s_lo; i < s_hi; ++i) {
+        const SeqTiles t = seq_tiles(a, i, TB);
+        const long cost = t.cost(t.MT, TB, fixed) * a.Hkv;
+        if (r < cost) {
+          found_s = i;
+          found_seq = t;
+          found_rem = r;
+          break;
+        }
+        r -= cost;
       }
-      r -= c;
     }
+    __syncthreads();
+    s = uni(found_s);
+    rem = uni(found_rem);
+    seq = uniform(found_seq);
   }
-  __syncthreads();
-  int s = uni(found_s);
-  long rem = uni(found_rem);
-  SeqTiles seq = uniform(found_seq);
   int h, mt;
   {
     const long per_head = seq.cost(seq.MT, TB, fixed);
@@ -698,13 +726,13 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
       __syncthreads();
       for (int i = tid; i < rows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c4 = i % (D / 4);
-        float mx = row_m[0][r];
+        float top = row_m[0][r];
 #pragma unroll
-        for (int k = 1; k < KW; ++k) mx = fmaxf(mx, row_m[k][r]);
+        for (int k = 1; k < KW; ++k) top = fmaxf(top, row_m[k][r]);
         float sum = 0.f, v0 = 0.f, v1 = 0.f, v2 = 0.f, v3 = 0.f;
 #pragma unroll
         for (int k = 0; k < KW; ++k) {
-          const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(row_m[k][r] - mx);
+          const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(row_m[k][r] - top);
           const float4 v = *reinterpret_cast<const float4*>(sm + k * 2 * C::STAGE + r * D * 4 + ((c4 ^ (r & 15)) * 16));
           sum += f * row_l[k][r];
           v0 += f * v.x; v1 += f * v.y; v2 += f * v.z; v3 += f * v.w;
@@ -715,11 +743,11 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
           const float f = sum > 0.f ? vs / sum : 0.f;
           *reinterpret_cast<uint2*>(a.out + at * D + 4 * c4) =
               make_uint2(pack_bf16x2(v0 * f, v1 * f), pack_bf16x2(v2 * f, v3 * f));
-          if (a.lse && c4 == 0) a.lse[at] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+          if (a.lse && c4 == 0) a.lse[at] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
         } else {
           *reinterpret_cast<float4*>(slot + (size_t)r * D + 4 * c4) = make_float4(v0, v1, v2, v3);
           if (c4 == 0) {
-            slot[C::M * D + r] = mx;
+            slot[C::M * D + r] = top;
             slot[C::M * D + C::M + r] = sum;
           }
         }
