@@ -364,7 +364,7 @@ typedef enum {
  *              outside [0, num_pages * page_size) (-1 for padding) is not cached. Two tokens
  *              with the same slot leave that slot's bytes undefined (and no others).
  *   q_out      [T, num_q_heads, head_dim] bf16 out, written for every token (NULL when
- *              num_q_heads == 0)
+ *              num_q_heads == 0); overlaps no input
  *   Float32 arithmetic and one rounding per value: bf16 (to nearest even), or e4m3 of
  *   value / scale (to nearest even, saturating at +-448; NaN stays NaN).
  *   limits: num_kv_heads >= 1, and those of moe_qk_norm_rope and of the cache. */
@@ -406,8 +406,8 @@ int moe_kv_append(const uint16_t* qkv, size_t qkv_stride, int T, int num_q_heads
  *   are rounded to the matrix cores' type: bf16 (2^-9 relative, as the output's own
  *   rounding), float16 for an e4m3 cache (2^-12); lse sums the unrounded ones.
  *   limits: those of the cache; num_q_heads a multiple of num_kv_heads, at most 128 times
- *   it, num_q_heads <= 1024; S <= 65536; max_pages * page_size < 2^30; scale > 0;
- *   softcap >= 0.
+ *   it, num_q_heads <= 1024; S <= 65536; max_pages * page_size < 2^30; 0 < scale <= 1e6;
+ *   softcap 0 or in 1e-6..1e6. out and lse overlap no input.
  * Results do not depend on scheduling: no atomics, sums in a fixed order. */
 int moe_tree_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
                        const float* k_scale, const float* v_scale, int num_pages, int page_size,

@@ -140,7 +140,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, int s, int TB) 
   t.row0 = q.row0;
   t.n = q.n;
   t.kv = q.kv;
-  t.ctx = q.kv - q.n;
+  t.ctx = q.kv - q.tokens;
   t.lo = a.tree_mask ? q.kv : (a.prefix_lens ? min(max(a.prefix_lens[s], 0), q.kv) : 0);
   t.MT = (q.n + TB - 1) / TB;
   return t;
@@ -431,7 +431,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
     }
     if (a.tree_mask) {
       lim = max(seq.ctx, 0);
-      word = a.tree_mask[qrow] & (~0ull >> (64 - seq.n));
+      word = a.tree_mask[qrow] & (~0ull >> (64 - min(seq.kv - seq.ctx, 64)));
     } else {
       lim = max(seq.lo, seq.ctx + tok0 + tok + 1);
       word = 0;
@@ -917,7 +917,8 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   // tile holds its whole query group
   const long segments = (long)a.Hkv * (KW == 1 ? a.T / TB : min(a.S, a.T));
   const long bound = (long)a.Hkv * ((a.T + TB - 1) / TB + a.S);
-  if (take_whole(KW == 1, segments, (long)a.max_pages << a.page_shift) && bound <= 1l << 22) {
+  // (every workgroup reads every sequence's lengths: not for thousands of sequences)
+  if (take_whole(KW == 1, segments, (long)a.max_pages << a.page_shift) && bound <= 1l << 22 && a.S <= 4096) {
     const int grid = (int)bound;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, true, 0, partials,
                        descs);

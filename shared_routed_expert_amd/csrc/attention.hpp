@@ -47,15 +47,17 @@ hipError_t launch_attention(const AttnArgs&, hipStream_t);
 size_t attention_workspace_bytes(int S, int max_q, int Hq, int Hkv, int D);
 
 // One sequence of an attention call, with every length taken from device memory held to
-// what the arrays can hold: first query row, query tokens, cached tokens.
+// what the arrays can hold: first query row, query tokens (of them the first max_q are computed),
+// cached tokens.
 struct SeqInfo {
-  int row0, n, kv;
+  int row0, tokens, n, kv;
 };
 __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int s) {
   SeqInfo q;
   const int lo = min(max(a.cu_q[s], 0), a.T), hi = min(max(a.cu_q[s + 1], 0), a.T);
   q.row0 = lo;
-  q.n = min(max(hi - lo, 0), a.max_q);
+  q.tokens = max(hi - lo, 0);
+  q.n = min(q.tokens, a.max_q);
   q.kv = min(max(a.kv_lens[s], 0), a.max_pages << a.page_shift);
   return q;
 }

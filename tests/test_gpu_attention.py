@@ -269,6 +269,28 @@ def test_fewer_cached_tokens_than_queries(which, wide):
     run_check(c, which, None, sees, wide=wide)
 
 
+@pytest.mark.parametrize("which", ["tree", "prefill"])
+def test_more_tokens_than_max_q(which):
+    """Only the first max_q tokens of a sequence are computed, at their own places in the cache."""
+    ns, kvs = [9, 40, 3], [50, 700, 3]
+    c = make_case(ns, kvs, 12, 1, 128, 16, False, seed=2)
+    sees = [oracle.visible_tree(n, k, None) for n, k in zip(ns, kvs)]
+    d = Dev(c)
+    d.max_q = 5
+    d.ws_bytes = L.moe_attention_workspace_bytes(3, c.T, 5, c.Hq, c.Hkv, c.D)
+    d.out.fill_(0x7FC1)
+    d.lse.fill_(7.0)
+    d.call(which)
+    torch.cuda.synchronize()
+    out, lse = bits_of(d.out).copy(), d.lse.cpu().numpy().copy()
+    for s, n in enumerate(ns):
+        a = int(c.cu_q[s])
+        ref, rl, mag, _ = oracle.attend(c.q_heads(s)[:5], c.k[s], c.v[s], sees[s][:5], 128 ** -0.5)
+        got = f32_from_bf16_bits(out[a:a + min(n, 5)].copy())
+        assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * mag)   # both roundings, and room for the sums
+        assert np.all(out[a + 5:a + n] == 0x7FC1) and np.all(lse[a + 5:a + n] == 7.0)
+
+
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("n", [1, 30])
 @pytest.mark.parametrize("fp8", [False, True])

@@ -60,7 +60,7 @@ def test_attention_rejects(L, which):
                dict(num_q_heads=12, num_kv_heads=5), dict(q_stride=12 * 128 - 8), dict(q_stride=12 * 128 + 4),
                dict(kv_type=3), dict(num_pages=0), dict(page_stride=2032), dict(page_stride=4104), dict(max_pages=0),
                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
-               dict(softcap=-1.0), dict(softcap=float("nan")), dict(kv_type=1), dict(kv_type=1, k_scale=FAKE)):
+               dict(scale=2e6), dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=1e-7), dict(softcap=1e7), dict(kv_type=1), dict(kv_type=1, k_scale=FAKE)):
         assert attention(L, which, **kw) == -1, kw
     for kw in (dict(head_dim=80), dict(page_size=8), dict(page_size=24), dict(S=65537), dict(num_pages=1 << 27),
                dict(num_q_heads=129, q_stride=1 << 20), dict(num_q_heads=2048, num_kv_heads=64, q_stride=1 << 20),
