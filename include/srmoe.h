@@ -378,7 +378,8 @@ int moe_kv_append(const uint16_t* qkv, size_t qkv_stride, int T, int num_q_heads
  * token r (kv head h / (num_q_heads / num_kv_heads)), over the cached tokens j it sees:
  *     z_j = scale * q_r.k_j, or softcap * tanh(scale * q_r.k_j / softcap) when softcap > 0
  *     lse[r,h] = log sum_j exp(z_j)      out[r,h,:] = sum_j exp(z_j - lse[r,h]) v_j
- * A row that sees nothing gets out = 0 and lse = -infinity.
+ * A row that sees nothing gets out = 0 and lse = -infinity. A NaN in a q head makes out and lse
+ * of that row NaN where it sees anything, and no other row's.
  *   q           token r's heads [num_q_heads, head_dim] bf16 at q + r * q_stride (q_stride >=
  *               num_q_heads * head_dim, a multiple of 8): q_out of moe_kv_append, or the
  *               q heads of a qkv row
@@ -403,8 +404,9 @@ int moe_kv_append(const uint16_t* qkv, size_t qkv_stride, int T, int num_q_heads
  * moe_prefill_attention: a chunk of a prompt. Token i sees the cached tokens j <= ctx + i, and
  *   those j < prefix_lens[s] (prefix_lens [S] int32, or NULL: none), j < kv_lens[s].
  *   Scores, softmax statistics and sums are float32. The weights exp(z - max) that multiply v
- *   are rounded to the matrix cores' type: bf16 (2^-9 relative, as the output's own
- *   rounding), float16 for an e4m3 cache (2^-12); lse sums the unrounded ones.
+ *   are rounded to the matrix cores' type: bf16 (by at most 2^-8 of the weight, as the output's
+ *   own rounding; where max_q * (num_q_heads / num_kv_heads) <= 32 they go as the sum of two
+ *   bf16, 2^-16), float16 for an e4m3 cache (2^-11); lse sums the unrounded ones.
  *   limits: those of the cache; num_q_heads a multiple of num_kv_heads, at most 128 times
  *   it, num_q_heads <= 1024; S <= 65536; max_pages * page_size < 2^30; 0 < scale <= 1e6;
  *   softcap 0 or in 1e-6..1e6. out and lse overlap no input.

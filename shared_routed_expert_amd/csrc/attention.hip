@@ -676,7 +676,8 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // before the stages are filled again
     }
 
-    // -------- the segment's result, or this part's partial
+    // -------- the segment's result, or this part's partial (a sum of 0: the row sees nothing; a NaN in
+    // q leaves a NaN sum, and NaN is what the row gets)
     const bool complete = begins && (ends || ntiles == 0);
     float* const slot = partials + (size_t)(2 * w + (begins ? 1 : 0)) * C::SLOT;
     if constexpr (KW == 1) {
@@ -686,7 +687,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
         if (complete) {
           const int tok = r / a.G, head = h * a.G + r - tok * a.G;
           const size_t at = (size_t)(row0 + tok) * a.Hq + head;
-          const float f = sum > 0.f ? vs / sum : 0.f;
+          const float f = sum != 0.f ? vs / sum : 0.f;
 #pragma unroll
           for (int d = 0; d < C::DT; ++d)
 #pragma unroll
@@ -694,7 +695,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
               *reinterpret_cast<uint2*>(a.out + at * D + 32 * d + 8 * i + 4 * half) =
                   make_uint2(pack_bf16x2(o[d][4 * i] * f, o[d][4 * i + 1] * f),
                              pack_bf16x2(o[d][4 * i + 2] * f, o[d][4 * i + 3] * f));
-          if (a.lse && half == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+          if (a.lse && half == 0) a.lse[at] = sum != 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
         } else {
 #pragma unroll
           for (int d = 0; d < C::DT; ++d)
@@ -740,10 +741,10 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
         if (complete) {
           const int tok = r / a.G, head = h * a.G + r - tok * a.G;
           const size_t at = (size_t)(row0 + tok) * a.Hq + head;
-          const float f = sum > 0.f ? vs / sum : 0.f;
+          const float f = sum != 0.f ? vs / sum : 0.f;
           *reinterpret_cast<uint2*>(a.out + at * D + 4 * c4) =
               make_uint2(pack_bf16x2(v0 * f, v1 * f), pack_bf16x2(v2 * f, v3 * f));
-          if (a.lse && c4 == 0) a.lse[at] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+          if (a.lse && c4 == 0) a.lse[at] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
         } else {
           *reinterpret_cast<float4*>(slot + (size_t)r * D + 4 * c4) = make_float4(v0, v1, v2, v3);
           if (c4 == 0) {
@@ -811,7 +812,7 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const int M, const 
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (pl[i] > 0.f) {   // an empty partial says nothing
+        if (pl[i] != 0.f) {   // an empty partial says nothing, one of NaN makes the row NaN
           const float mn = fmaxf(m, pm[i]);
           const float f = __builtin_amdgcn_exp2f(m - mn), e = __builtin_amdgcn_exp2f(pm[i] - mn);
           m = mn;
@@ -847,10 +848,10 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const int M, const 
     if (p0 == 0 && base + g / side < d.rows) {
       const int tok = r / a.G;
       const size_t at = (size_t)(d.row0 + tok) * a.Hq + d.head * a.G + r - tok * a.G;
-      const float f = l > 0.f ? vs / l : 0.f;
+      const float f = l != 0.f ? vs / l : 0.f;
       *reinterpret_cast<uint2*>(a.out + at * D + 4 * c4) =
           make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-      if (a.lse && c4 == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (a.lse && c4 == 0) a.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
   }
 }

@@ -294,6 +294,27 @@ def test_more_tokens_than_max_q(which):
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("n", [1, 30])
 @pytest.mark.parametrize("fp8", [False, True])
+def test_a_nan_in_q_stays_in_its_row(fp8, n, wide):
+    """Whole segments and split ones: the row's out and lse are NaN, the other rows within the bars."""
+    c = make_case([n, n], [700, 3000], 12, 1, 128, 16, fp8, seed=4)
+    sees = [oracle.visible_tree(n, k, None) for k in c.kvs]
+    clean = run_check(c, "tree", None, sees, wide=wide)
+    tok, head = 2 * n - 1, 5
+    row, row_lse = clean.out[tok, head].clone(), clean.lse[tok, head].clone()
+    d = Dev(c)
+    d.out.fill_(0x7FC1)
+    d.lse.fill_(7.0)
+    d.q[tok, head * 128 + 77] = 0x7FC1
+    d.call("tree")
+    torch.cuda.synchronize()
+    assert bool(d.out[tok, head].view(torch.bfloat16).isnan().all()) and bool(d.lse[tok, head].isnan())
+    d.out[tok, head], d.lse[tok, head] = row, row_lse
+    check(c, bits_of(d.out), d.lse.cpu().numpy(), sees, 128 ** -0.5, 0.0)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("n", [1, 30])
+@pytest.mark.parametrize("fp8", [False, True])
 def test_pages_outside_the_pool_are_unseen(fp8, n, wide):
     c = make_case([n, n], [200, 90], 12, 1, 128, 16, fp8, seed=3)
     c.table[0, 2], c.table[0, 7], c.table[1, 0] = -1, c.kv.shape[0], 2 ** 31 - 1
