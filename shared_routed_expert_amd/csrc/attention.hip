@@ -642,7 +642,17 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
         }
       }
     } else {
-      // the waves share a tile: loaded one tile ahead into the other stage, one barrier per tile
+      // the waves share a tile: loaded one tile ahead into the other stage, one barrier per tile.
+      // Matrix work goes ahead of the other workgroup's vector work (16384 tokens over e4m3: 864 -> 843 us).
+      // bf16: the odd wave slot of a SIMD (hardware id, low bit) ahead of the even one as well, since two that
+      // share the matrix core in turn also end together and then want the vector unit together (a prompt of
+      // 4096 tokens 84 -> 81 us, of 96 heads 474 -> 460, 16384 tokens at D = 64 370 -> 355; over e4m3,
+      // where conversions keep the vector unit busy, 867 -> 883).
+      const bool ahead = !FP8 && (__builtin_amdgcn_s_getreg(4 | 3 << 11) & 1);
+      auto matrix_work = [&]() {
+        if (ahead) __builtin_amdgcn_s_setprio(3);
+        else __builtin_amdgcn_s_setprio(1);
+      };
       if (t0 < t1) {
         pages_for(t0 * NK);
         issue(kc, stages_off, t0 * NK);
@@ -661,15 +671,14 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
           issue(kc, nx, (t + 1) * NK);
           issue(vc, nx + C::TILE, (t + 1) * NK);
         }
-        // matrix work ahead of the other workgroup's vector work (16384 tokens over e4m3: 864 -> 843 us)
-        __builtin_amdgcn_s_setprio(1);
+        matrix_work();
         scores(st);
         __builtin_amdgcn_s_setprio(0);
         mask(t * NK);
         maxima();
         move_max();
         weights();
-        __builtin_amdgcn_s_setprio(1);
+        matrix_work();
         values(st + C::TILE);
         __builtin_amdgcn_s_setprio(0);
       }
