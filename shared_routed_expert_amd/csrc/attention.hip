@@ -24,7 +24,8 @@
 // Two arrangements of a workgroup's waves:
 //   RW == 1 (decode, small trees): every wave walks keys of its own through its own two LDS
 //     stages, with no barrier; the KW waves' sums are joined at the end of the segment.
-//   KW == 1 (larger trees, prompts): RW waves with rows of their own share each key tile.
+//   KW == 1 (larger trees, prompts): RW waves with rows of their own share each key tile; two such
+//     workgroups per CU, one's matrix work beside the other's vector work.
 //
 // Work split. The segments of all sequences, heads and row tiles are laid end to end, each as
 // long as the keys it sees; workgroup w takes the w-th of equal parts of that line, so ragged
@@ -200,13 +201,17 @@ struct Attn {
   static constexpr int kSegCost = RW == 1 ? 192 : 256;
   static constexpr int kMinPart = RW == 1 ? KW * NK : 4 * NK;   // a part's cost in keys is at least this
   static constexpr int SLOT = M * D + 2 * M;    // floats of a partial: O [M][D], then m and l per row
+  // Shared tiles of D = 256: q and O^T alone are 192 of the 256 registers that two workgroups per CU leave
+  // (a chunk of 8192 tokens of 8 heads: bf16 352 us, one workgroup 475; e4m3 330 and 440). LDS is then
+  // read fewer products ahead and its addresses are formed anew for each tile; kept, they spill.
+  static constexpr bool kTight = RW == 4 && D == 256;
   static_assert(NX % RW == 0 && RPI <= 16 && NK <= 64, "tile shape");
   static_assert(KW == 1 || M * D * 4 <= 2 * STAGE, "the waves' sums are joined in their stages");
 };
 
 template <int D, bool FP8, int RW, int KW, int NK, bool CAP>
 __global__ void __launch_bounds__(64 * RW * KW)
-__attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 256 ? 2 : 1))) attention_kernel(
+__attribute__((amdgpu_waves_per_eu(RW == 4 ? 2 : 1, RW == 4 ? 2 : 1))) attention_kernel(
     const AttnArgs a, const int TB, const int parts_max, const bool whole, const int desc_tiles,
     float* __restrict__ partials, PartDesc* __restrict__ descs) {
   using C = Attn<D, FP8, RW, KW, NK, CAP>;
@@ -458,7 +463,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
 #pragma unroll
       for (int t = 0; t < C::KT; ++t) sc[t] = v16f{};
       constexpr int kReads = C::KT * C::STEPS / (FP8 ? 2 : 1);   // 16 bytes: one step of bf16, two of e4m3
-      constexpr int kAhead = FP8 ? 3 : 6;
+      constexpr int kAhead = C::kTight ? (FP8 ? 2 : 3) : (FP8 ? 3 : 6);
       i32x4 raw[kReads];
       auto read = [&](int i) {
         const int t = i % C::KT, st = i / C::KT;
@@ -564,7 +569,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
 
     auto values = [&](const uint8_t* v) {
       constexpr int kReads = NK / 16 * C::DT;
-      constexpr int kAhead = 4;
+      constexpr int kAhead = C::kTight ? 2 : 4;
       i32x4 raw[kReads];
       auto read = [&](int i) {
         const int st = i / C::DT, d = i % C::DT;
@@ -662,6 +667,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 && D < 256 ? 2 : 1, RW == 4 && D < 25
       for (int t = t0; t < t1; ++t) {
         const int b = (t - t0) & 1;
         uint8_t* const st = stages + b * C::STAGE;
+        if constexpr (C::kTight) asm volatile("" : "+v"(k_addr), "+v"(v_addr), "+v"(v_addr2));
         wait_vm<0>();
         if ((t + 1) * NK > seq.kv || careful) zero_rows(st + C::TILE, t * NK);
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -888,9 +894,16 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 }
 
 // ------------------------------------------------------------------------------------- the launch
-// Parts of the line of segments = workgroups, all resident at once: one per CU (256), or two where
-// the register file and LDS hold two (128-row tiles of head_dim 64 and 128)
-constexpr int parts_of(int M, int D) { return M == 128 && D < 256 ? 512 : 256; }
+// Parts of the line of segments = workgroups, all resident at once: one per CU (256), or two with shared
+// tiles. One per CU there too where a part would see few keys, for half the partials: `segments` at most
+// of at most `keys` keys. One and two per CU measured, by keys per part of two: 275 44 and 51 us (one
+// prompt of 1500 tokens, D = 256), 450 29.8 and 31.7 (trees of 64 tokens), 512 46 and 55 (trees of 20 tokens,
+// D = 256), 1125 41 and 42 (trees of 16 tokens, e4m3), 2048 67 and 60 (trees of 5 tokens, 96 heads), 3280 101 and 85
+// (one prompt of 4096 tokens).
+constexpr int parts_of(int M) { return M == 128 ? 512 : 256; }
+static int parts_for(int M, long segments, long keys) {
+  return M == 128 && segments * keys < 512l * 1024 ? 256 : parts_of(M);
+}
 
 // Whether a workgroup takes a whole segment (no partials, no join) rather than an equal part of the
 // line: `segments` as the rows of q say, `keys` as the block table allows at most. Whole and split
@@ -912,14 +925,14 @@ static size_t slot_floats(int M, int D) { return (size_t)M * D + 2 * M; }
 size_t attention_workspace_bytes(int S, int max_q, int Hq, int Hkv, int D) {
   (void)S;
   const int M = tile_rows(max_q, Hq / Hkv);
-  return parts_of(M, D) * 2 * (slot_floats(M, D) * 4 + sizeof(PartDesc));
+  return parts_of(M) * 2 * (slot_floats(M, D) * 4 + sizeof(PartDesc));
 }
 
 template <int D, bool FP8, int RW, int KW, int NK, bool CAP>
 static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   using C = Attn<D, FP8, RW, KW, NK, CAP>;
   auto* kernel = attention_kernel<D, FP8, RW, KW, NK, CAP>;
-  constexpr int kParts = parts_of(C::M, D);
+  constexpr int kParts = parts_of(C::M);
   float* partials = static_cast<float*>(a.ws);
   PartDesc* descs = reinterpret_cast<PartDesc*>(partials + 2 * kParts * slot_floats(C::M, D));
   const int TB = C::M / a.G;
@@ -927,8 +940,9 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   // tile holds its whole query group
   const long segments = (long)a.Hkv * (KW == 1 ? a.T / TB : min(a.S, a.T));
   const long bound = (long)a.Hkv * ((a.T + TB - 1) / TB + a.S);
+  const long keys = (long)a.max_pages << a.page_shift;
   // (every workgroup reads every sequence's lengths: not for thousands of sequences)
-  if (take_whole(KW == 1, segments, (long)a.max_pages << a.page_shift) && bound <= 1l << 22 && a.S <= 4096) {
+  if (take_whole(KW == 1, segments, keys) && bound <= 1l << 22 && a.S <= 4096) {
     const int grid = (int)bound;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, true, 0, partials,
                        descs);
@@ -936,15 +950,16 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   }
   const int tiles = (a.max_q + TB - 1) / TB;
   const long most = (long)a.S * a.Hkv * tiles;   // segments, if every sequence had max_q tokens
+  const int parts = parts_for(C::M, min(most, bound), keys);
   const bool by_segment = most <= 2 * kParts;
-  hipLaunchKernelGGL(kernel, dim3(kParts), dim3(64 * C::kWaves), C::LDS, stream, a, TB, kParts, false,
+  hipLaunchKernelGGL(kernel, dim3(parts), dim3(64 * C::kWaves), C::LDS, stream, a, TB, parts, false,
                      by_segment ? tiles : 0, partials, descs);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // about as many workgroups as are resident at once, and no more than a segment has rows
   const int rows = (int)min((long)C::M, (long)a.max_q * a.G);
   const int y = by_segment ? max(1, min((int)(2048 / most), min(rows, 32))) : 4;
-  hipLaunchKernelGGL(attention_join_kernel<D>, dim3(by_segment ? (int)most : kParts, y), dim3(kJoinThreads), 0,
+  hipLaunchKernelGGL(attention_join_kernel<D>, dim3(by_segment ? (int)most : parts, y), dim3(kJoinThreads), 0,
                      stream, a, C::M, TB, by_segment ? tiles : 0, (const float*)partials, (const PartDesc*)descs);
   return hipGetLastError();
 }
