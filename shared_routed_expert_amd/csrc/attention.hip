@@ -32,6 +32,11 @@
 // batches and causal triangles balance without a host-side plan. A segment that spans several
 // parts leaves one partial (O, m, l) per part in the workspace, joined by a second kernel in
 // part order (no atomics; the same bits every time).
+//
+// What bounds it, measured (one call, join included). Decode: bytes; 24 sequences of up to 16384 tokens on 8 kv
+// heads 151 us (0.93 GB, 6.1 TB/s), 64 of up to 8192 on one 35 us (160 MB). Prompts: the matrix cores and
+// the vector unit in turn; 16384 tokens of 12 heads 838 us (983 TFLOP/s), over e4m3 860, 4096 tokens 78 us. Small
+// calls: latency; one sequence of 777 tokens 13 us, 8 trees of 64 tokens over up to 4099 26 us.
 #include "attention.hpp"
 #include "common.hpp"
 
@@ -799,6 +804,8 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 ? 2 : 1, RW == 4 ? 2 : 1))) attention
 // each); the workgroup's groups of such lanes stand side by side on `side` partials of a row (few
 // partials: on rows of their own), and each has kBatch of them in flight, so that neither a segment
 // split over the whole card nor 128 rows of two partials each wait for memory more than a few times.
+// Bound by a launch and its tail (64 sequences, 3 MB: 4.6 us), then bytes (one prompt of 4096 tokens, 59 MB: 11.8
+// us, 5.0 TB/s).
 constexpr int kJoinThreads = 256;
 template <int D, int kBatch>
 __device__ __forceinline__ void join_rows(const AttnArgs& a, const int M, const PartDesc& d, const int side,

@@ -340,6 +340,17 @@ def test_many_sequences(wide):
     run_check(c, "tree", None, [oracle.visible_tree(1, k, None) for k in kvs], wide=wide)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [1, 20])
+def test_thousands_of_sequences(n, fp8):
+    """More sequences than threads, some without tokens: every part finds its own among them."""
+    rng = np.random.default_rng(1)
+    ns = [int(x) for x in rng.integers(0, n + 1, 5000)]
+    kvs = [int(x) for x in rng.integers(0, 40, 5000)]
+    c = make_case(ns, kvs, 2, 1, 64, 16, fp8, seed=7)
+    run_check(c, "tree", None, [oracle.visible_tree(a, k, None) for a, k in zip(ns, kvs)])
+
+
 def test_same_bits_every_time():
     for which, ns, kvs in (("tree", [1] * 5, [40000, 3, 999, 2000, 17]), ("tree", [40, 64], [3000, 64]),
                            ("prefill", [700, 100], [900, 2000])):
