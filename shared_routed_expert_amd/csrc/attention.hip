@@ -204,7 +204,7 @@ struct Attn {
   // What a segment costs besides its keys, in keys (its q, its first tile's latency, its result: about
   // 5 us, a tile of 64 keys 1.2 to 1.7)
   static constexpr int kSegCost = RW == 1 ? 192 : 256;
-  static constexpr int kMinPart = RW == 1 ? KW * NK : 4 * NK;   // a part's cost in keys is at least this
+  static constexpr int kMinPart = RW == 1 ? (KW < 4 ? 64 : 128) : 4 * NK;   // a part's cost in keys is at least this
   static constexpr int SLOT = M * D + 2 * M;    // floats of a partial: O [M][D], then m and l per row
   // Shared tiles of D = 256: q and O^T alone are 192 of the 256 registers that two workgroups per CU leave
   // (a chunk of 8192 tokens of 8 heads: bf16 352 us, one workgroup 475; e4m3 330 and 440). LDS is then
@@ -216,7 +216,7 @@ struct Attn {
 
 template <int D, bool FP8, int RW, int KW, int NK, bool CAP>
 __global__ void __launch_bounds__(64 * RW * KW)
-__attribute__((amdgpu_waves_per_eu(RW == 4 ? 2 : 1, RW == 4 ? 2 : 1))) attention_kernel(
+__attribute__((amdgpu_waves_per_eu(RW == 4 || KW == 8 ? 2 : 1, RW == 4 || KW == 8 ? 2 : 1))) attention_kernel(
     const AttnArgs a, const int TB, const int parts_max, const bool whole, const int desc_tiles,
     float* __restrict__ partials, PartDesc* __restrict__ descs) {
   using C = Attn<D, FP8, RW, KW, NK, CAP>;
@@ -973,8 +973,13 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
 
 template <int D, bool FP8, bool CAP>
 static hipError_t launch_rows(const AttnArgs& a, hipStream_t stream) {
-  constexpr int NKs = FP8 || D == 64 ? (D == 256 ? 32 : 64) : 32;
-  if (tile_rows(a.max_q, a.G) == 32) return launch_one<D, FP8, 1, D == 256 ? 2 : 4, NKs, CAP>(a, stream);
+  // A wave's own keys: as many waves as LDS holds two stages for, two per SIMD where that is eight, so that one
+  // converts and exponentiates beside the other's loads (e4m3, eight waves of 32 keys and four of 64: 64
+  // sequences of up to 8192 27.3 and 30.0 us, 3 of 131072 30.9 and 34.2; D = 64, 64 sequences, 2 kv heads, bf16 37.7 and
+  // 39.3; D = 256, four of 32 keys and two: 41.4 and 48.6).
+  constexpr int NKs = FP8 && D == 64 ? 64 : 32;
+  constexpr int KWs = D == 64 || (FP8 && D == 128) ? 8 : (FP8 || D == 128 ? 4 : 2);
+  if (tile_rows(a.max_q, a.G) == 32) return launch_one<D, FP8, 1, KWs, NKs, CAP>(a, stream);
   return launch_one<D, FP8, 4, 1, D == 256 ? 32 : 64, CAP>(a, stream);
 }
 
