@@ -204,7 +204,9 @@ struct Attn {
   // What a segment costs besides its keys, in keys (its q, its first tile's latency, its result: about
   // 5 us, a tile of 64 keys 1.2 to 1.7)
   static constexpr int kSegCost = RW == 1 ? 192 : 256;
-  static constexpr int kMinPart = RW == 1 ? (KW < 4 ? 64 : 128) : 4 * NK;   // a part's cost in keys is at least this
+  // A part's cost in keys is at least this (eight waves, 128 and 256: 20 sequences of 2 tokens over up to
+  // 3000 keys 17.5 and 20 us, 20 of 3000 keys 19.4 and 16.5, one of 3000 15.3 and 14.8)
+  static constexpr int kMinPart = RW == 1 ? (KW < 4 ? 64 : 128) : 4 * NK;
   static constexpr int SLOT = M * D + 2 * M;    // floats of a partial: O [M][D], then m and l per row
   // Shared tiles of D = 256: q and O^T alone are 192 of the 256 registers that two workgroups per CU leave
   // (a chunk of 8192 tokens of 8 heads: bf16 352 us, one workgroup 475; e4m3 330 and 440). LDS is then
