@@ -822,7 +822,7 @@ static int attention(const uint16_t* q, size_t q_stride, const void* k_cache, co
   if (st != SRMOE_OK) return st;
   st = check_cache_dims(kv_type, num_kv_heads, head_dim, num_pages, page_size, page_stride);
   if (st != SRMOE_OK) return st;
-  // (the cap's reciprocal and the scale's multiples stay finite in float32)
+  // (the cap's reciprocal and the scale's multiples stay finite in float32; the kernels hold a factor that underflows)
   if (max_pages < 1 || !(scale > 0.f) || !(scale <= 1e6f) || !(softcap == 0.f || (softcap >= 1e-6f && softcap <= 1e6f)))
     return SRMOE_ERR_INVALID_ARG;
   if ((size_t)max_pages * page_size >= ((size_t)1 << 30)) return SRMOE_ERR_UNSUPPORTED;

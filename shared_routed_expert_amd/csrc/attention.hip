@@ -386,7 +386,9 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 || KW == 8 ? 2 : 1, RW == 4 || KW == 
     const int tok0 = mt * TB, rows = min(TB, seq.n - tok0) * a.G;
     const int row0 = seq.row0 + tok0;
     const float ks = FP8 ? a.k_scale[h] : 1.f, vs = FP8 ? a.v_scale[h] : 1.f;
-    const float c = CAP ? 2.f * kLog2e * a.scale * ks / a.softcap : scale2 * ks;
+    // Not 0 where scale * ks underflows: a masked score of -inf times 0 would be NaN. The smallest float32 instead moves
+    // a score by less than 2^-21 whatever q.k is.
+    const float c = CAP ? 2.f * kLog2e * a.scale * ks / a.softcap : fmaxf(scale2 * ks, 0x1p-149f);
     const float cap2 = a.softcap * kLog2e, half_cap = 0.5f * a.softcap;
     const int* table = a.block_table + (size_t)s * a.max_pages;
     const int pages_used = (seq.kv + page_mask) >> a.page_shift;

@@ -1,4 +1,4 @@
-"""Scores at the ends of their range: caps from the smallest to the largest that the calls accept, on every
+"""Scores at the ends of their range: caps and scales from the smallest to the largest that the calls accept, on every
 kernel variant that caps, against the float64 oracle.
 
 Bars, with A, X, u as in test_gpu_attention (A = sum_j w_j |v_j|, X the row's largest sum_d |q_d k_d| * scale, u the
@@ -90,3 +90,18 @@ def test_capped_trees(Hq, Hkv, D, n, fp8, cap):
     words[0][0] = 0
     run_scores(c, "tree", np.concatenate(words).view(np.int64), [oracle.visible_tree(n, k, w) for k, w in zip(kvs, words)],
                D ** -0.5, cap, "caps")
+
+
+@pytest.mark.parametrize("cap", [0.0, 1.0])
+@pytest.mark.parametrize("scale,k_factor", [(1e-45, 1.0), (1e-44, 1.0), (1e-38, 1.0), (1e-15, 2.0 ** -100), (1e-20, 1.0)])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [1, 70])
+def test_tiny_scales(n, fp8, scale, k_factor, cap):
+    """Scores so small that their factor (scale times the keys' own) is zero in float32: every seen token has the same
+    weight, and the masked ones still none."""
+    kvs = [n, 77 + n, 200]
+    c = make_case([n] * 3, kvs, 12, 1, 128, 16, fp8, seed=n)
+    if fp8:
+        c.scales[0] *= np.float32(k_factor)
+        c.k = [k * k_factor for k in c.k]
+    run_scores(c, "prefill", None, [oracle.visible_prefill(n, k, 0) for k in kvs], scale, cap, "tiny scales")
