@@ -111,13 +111,12 @@ enum Cap { kCapNone, kCapSmall, kCapLarge };
 // sequences of up to 16384 tokens, 0.93 GB: 170 us without, 152 us with).
 template <bool kOnce>
 __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t voff, const uint8_t* base) {
+  // (the LDS address goes in as m0 itself, so that the compiler knows what the register holds; a wait state after it)
   if (kOnce)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(uni((int)lds)), "v"(voff),
-                 "s"(uni((long)base))
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"{m0}"(uni((int)lds)), "v"(voff), "s"(uni((long)base))
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uni((int)lds)), "v"(voff),
-                 "s"(uni((long)base))
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(uni((int)lds)), "v"(voff), "s"(uni((long)base))
                  : "memory");
 }
 
