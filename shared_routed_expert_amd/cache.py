@@ -102,7 +102,7 @@ class PagedKVCache:
         self._tensor(cu_q, "cu_q", torch.int32, (S + 1,))
         self._tensor(kv_lens, "kv_lens", torch.int32, (S,))
         if out is None:
-            out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            out = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device=q.device)   # rows of no sequence are not written
         self._tensor(out, "out", torch.bfloat16, (T, Hq, D))
         if lse is not None:
             self._tensor(lse, "lse", torch.float32, (T, Hq))
@@ -118,7 +118,8 @@ class PagedKVCache:
                        lse=None):
         """Attention of each sequence's last tokens (drafted ones: tree_mask [T] int64 words, bit b = the sequence's
         drafted token b is seen; None: a chain, with one token per sequence ordinary decoding) over its cached tokens.
-        scale: head_dim^-1/2 unless given. Returns out [T, q heads, head_dim]."""
+        scale: head_dim^-1/2 unless given. Returns out [T, q heads, head_dim]; rows outside every sequence and a
+        sequence's tokens past max_q are zero, or left as they were in an out (and lse) that is given."""
         if tree_mask is not None:
             self._tensor(tree_mask, "tree_mask", torch.int64, (q.shape[0],))
         return self._attention(L.moe_tree_attention, q, block_table, cu_q, kv_lens, tree_mask, max_q, scale, softcap, out,
@@ -127,7 +128,8 @@ class PagedKVCache:
     def prefill_attention(self, q, block_table, cu_q, kv_lens, max_q, prefix_lens=None, scale=None, softcap=0.0, out=None,
                           lse=None):
         """Causal attention of a chunk's tokens over the cached tokens, its own among them (append first);
-        prefix_lens [S]: every token also sees its sequence's first prefix_lens[s] tokens."""
+        prefix_lens [S]: every token also sees its sequence's first prefix_lens[s] tokens. scale, out, lse and the rows
+        outside every sequence as in tree_attention."""
         if prefix_lens is not None:
             self._tensor(prefix_lens, "prefix_lens", torch.int32, (block_table.shape[0],))
         return self._attention(L.moe_prefill_attention, q, block_table, cu_q, kv_lens, prefix_lens, max_q, scale, softcap,
