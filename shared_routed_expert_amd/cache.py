@@ -2,7 +2,8 @@
 
 Torch provides device memory and the stream (always torch's current stream of the cache's device); the
 writes (moe_kv_append) and the attention (moe_tree_attention, moe_prefill_attention) run in
-libsrmoe.so's HIP kernels.
+libsrmoe.so's HIP kernels. Every tensor starts on a 16-byte boundary, as torch allocates them; a slice that does not is
+refused by name.
 """
 from __future__ import annotations
 
@@ -14,6 +15,11 @@ from . import _lib as L
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
+
+
+def _need_aligned(t, name):
+    # every pointer that the library takes; said here, where the tensor has a name
+    _need(t.data_ptr() % 16 == 0, f"{name} starts on a 16-byte boundary (clone a slice that does not)")
 
 
 class PagedKVCache:
@@ -30,10 +36,12 @@ class PagedKVCache:
         self.kv_type = kv_type
         self.k_scale = self.v_scale = None
         if kv_type == L.KV_E4M3:
-            for t in (k_scale, v_scale):
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
                 _need(isinstance(t, torch.Tensor) and t.dtype == torch.float32 and tuple(t.shape) == (num_kv_heads,),
                       "an e4m3 cache needs k_scale and v_scale, float32 [num_kv_heads]")
-            self.k_scale, self.v_scale = k_scale.to(dev).contiguous(), v_scale.to(dev).contiguous()
+                t = t.to(dev).contiguous()
+                _need_aligned(t, name)
+                setattr(self, name, t)
         dtype = torch.bfloat16 if kv_type == L.KV_BF16 else torch.float8_e4m3fn
         self.kv = torch.empty((num_pages, 2, num_kv_heads, page_size, head_dim), dtype=dtype, device=dev)
         self.num_pages, self.page_size = num_pages, page_size
@@ -52,6 +60,7 @@ class PagedKVCache:
               f"{name} is {dtype} {list(shape)}")
         _need(strided or t.is_contiguous(), f"{name} is contiguous")
         _need(t.device == self.kv.device, f"{name} is on the cache's device")
+        _need_aligned(t, name)
         return t
 
     def _run(self, call, *args):
@@ -70,6 +79,7 @@ class PagedKVCache:
         T = qkv.shape[0]
         self._tensor(qkv, "qkv", torch.bfloat16, (T, (Hq + 2 * Hkv) * D), strided=True)
         _need(qkv.stride(1) == 1, "a row of qkv is contiguous")
+        _need(T < 2 or qkv.stride(0) % 8 == 0, "rows of qkv are a multiple of 8 values apart")
         self._tensor(slots, "slots", torch.int32, (T,))
         rd = max_pos = 0
         if cos_sin is not None:
@@ -96,6 +106,7 @@ class PagedKVCache:
         T, Hq = q.shape[:2]
         self._tensor(q, "q", torch.bfloat16, (T, Hq, D), strided=True)
         _need(q.stride(2) == 1 and (q.stride(1) == D or Hq == 1), "a token's heads are contiguous in q")
+        _need(T < 2 or q.stride(0) % 8 == 0, "rows of q are a multiple of 8 values apart")
         _need(isinstance(block_table, torch.Tensor) and block_table.dim() == 2, "block_table is int32 [S, max_pages]")
         S, max_pages = block_table.shape
         self._tensor(block_table, "block_table", torch.int32, (S, max_pages))
