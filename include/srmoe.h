@@ -406,7 +406,8 @@ int moe_kv_append(const uint16_t* qkv, size_t qkv_stride, int T, int num_q_heads
  *   Scores, softmax statistics and sums are float32. The weights exp(z - max) that multiply v
  *   are rounded to the matrix cores' type: bf16 (by at most 2^-8 of the weight, as the output's
  *   own rounding; where max_q * (num_q_heads / num_kv_heads) <= 32 they go as the sum of two
- *   bf16, 2^-16), float16 for an e4m3 cache (2^-11); lse sums the unrounded ones.
+ *   bf16, 2^-16), float16 for an e4m3 cache (2^-11 of the weight, or 2^-32 of the row's largest
+ *   weight where that is more); lse sums the unrounded ones.
  *   The cap adds a rounding of 2^-19 of the capped score, and of 2^-22 of a softcap up to 64.
  *   limits: those of the cache; num_q_heads a multiple of num_kv_heads, at most 128 times
  *   it, num_q_heads <= 1024; S <= 65536; max_pages * page_size < 2^30; 0 < scale <= 1e6;

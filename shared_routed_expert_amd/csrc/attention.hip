@@ -14,8 +14,9 @@
 // operand of O^T += V^T P^T when the keys of a 16-key step are counted as (half h of the wave,
 // j < 8) -> key 8 (j / 4) + 4 h + j % 4; V's transposing LDS reads fetch them in that order.
 //   m' = max(m, max z),  O' = O 2^(m - m') + sum 2^(z - m') v,  l' = l 2^(m - m') + sum 2^(z - m')
-// (z in units of log2 e). m only moves when a score exceeds it by more than 2^8: until then
-// the weights are at most 2^8, which float32 sums and both 16-bit types hold.
+// (z in units of log2 e). m only moves when a score exceeds it by more than 8: until then the
+// weights are at most 2^8 in bf16. In float16 they are 2^7 larger, so that the row's largest is 2^7 to
+// 2^15 (float16 ends below 2^16) and its subnormals, 2^-24 apart, lose at most 2^-32 of the largest weight.
 //
 // Keys and values go to LDS straight from global memory (16 bytes a lane), 16-byte chunks swapped
 // within a row by the source address (chunk c of key k sits at c ^ swizzle(k)), so that both
@@ -53,6 +54,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kMoveMax = 8.0f;    // a running maximum moves when a score exceeds it by this (base 2)
+constexpr float kHalfBias = 7.0f;   // float16 weights are 2^this larger
+static_assert(kMoveMax + kHalfBias <= 15.0f, "the largest weight is a finite float16");
 
 // 16-byte chunk swap of key k's row (CPR chunks of it), for LDS's 64 banks of 4 bytes: 16 consecutive
 // keys' same chunk (a step of K's reads) and the 64 or 32 bytes of {4h..4h+3} (8-bit: and 8+4h..) of a
@@ -348,7 +351,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 || KW == 8 ? 2 : 1, RW == 4 || KW == 
   const int page_mask = (1 << a.page_shift) - 1;
   const size_t page_bytes = a.page_stride * C::ES;
   const float scale2 = a.scale * kLog2e;
-  constexpr float kBias = FP8 ? 7.0f : 0.0f;   // float16 weights: 2^7 keeps small ones off its subnormals
+  constexpr float kBias = FP8 ? kHalfBias : 0.0f;
 
   // -------- this wave's LDS read addresses (see the layout above)
   int k_addr, v_addr, v_addr2;
