@@ -77,3 +77,45 @@ def test_captured_calls_of_the_object():
         got = bits_of(out.view(torch.int16)).copy()
         assert np.array_equal(got, bits_of(call().view(torch.int16))), kvs
         assert not got[3:].any() and got[:3].any(axis=(1, 2)).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cap", [0.0, 25.0])
+def test_options_of_the_object(fp8, cap):
+    """prefix_lens, tree_mask, a scale, a cap, out and lse of the caller's own, q as a slice of wider rows."""
+    ns, kvs, pre = [30, 64, 2], [200, 64, 91], [50, 0, 91]
+    c = make_case(ns, kvs, 12, 1, 128, 16, fp8, seed=3, q_extra=24)
+    cache, q, scale = cache_of(c), q_of(c), 0.05
+    assert not q.is_contiguous()
+    lens = up(np.array(kvs, np.int32))
+    words = [random_tree(n, np.random.default_rng(n)) for n in ns]
+    for call, extra, sees in (
+            (cache.prefill_attention, dict(prefix_lens=up(np.array(pre, np.int32))),
+             [oracle.visible_prefill(n, k, p) for n, k, p in zip(ns, kvs, pre)]),
+            (cache.tree_attention, dict(tree_mask=up(np.concatenate(words).view(np.int64))),
+             [oracle.visible_tree(n, k, w) for n, k, w in zip(ns, kvs, words)])):
+        out = torch.empty((c.T, 12, 128), dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty((c.T, 12), device=DEV)
+        got = call(q, up(c.table), up(c.cu_q), lens, 64, scale=scale, softcap=cap, out=out, lse=lse, **extra)
+        torch.cuda.synchronize()
+        assert got is out
+        check_rows(c, bits_of(out.view(torch.int16)), lse.cpu().numpy(), sees, float(np.float32(scale)), cap)
+
+
+def test_on_another_stream():
+    """The calls go to torch's current stream: behind the work that made their inputs, with nothing on the default one."""
+    c = make_case([1, 1], [900, 40], 12, 1, 128, 16, False, seed=5)
+    cache, table, cu, lens = cache_of(c), up(c.table), up(c.cu_q), up(np.array(c.kvs, np.int32))
+    src, q = q_of(c).contiguous(), torch.zeros((2, 12, 128), dtype=torch.bfloat16, device=DEV)
+    want = bits_of(cache.tree_attention(src, table, cu, lens, 1).view(torch.int16)).copy()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    big = torch.randn((4096, 4096), device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for _ in range(4):
+            big = big @ big * 1e-3
+        q.copy_(src)
+        out = cache.tree_attention(q, table, cu, lens, 1)
+    stream.synchronize()
+    assert np.array_equal(bits_of(out.view(torch.int16)), want)
