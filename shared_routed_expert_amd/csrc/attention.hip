@@ -178,6 +178,10 @@ __device__ __forceinline__ SeqTiles uniform(SeqTiles t) {
   return t;
 }
 
+// How the segments are shared out: equal parts of the line, whole segments, or either by the lengths that the
+// kernel finds (a launch of both: as many workgroups as there can be segments, and the join).
+enum Share { kEqualParts, kWholeSegments, kByLengths };
+
 // A segment that begins in part `first` and ends in a later part `last` (rows == 0: nothing to join)
 struct alignas(32) PartDesc {
   int row0, rows, head, first, last;
@@ -188,6 +192,9 @@ __device__ __forceinline__ long div_pos(long a, long b) {
   if (((uint64_t)(a | b) >> 32) == 0) return (long)((uint32_t)a / (uint32_t)b);
   return a / b;
 }
+
+// Workgroups that are resident at once with tiles of M rows, and so the most parts of the line
+constexpr int parts_of(int M) { return M == 128 ? 512 : 256; }
 
 // Part w of `parts` covers [begin(w), begin(w + 1)) of `total` units.
 struct Parts {
@@ -239,12 +246,13 @@ struct Attn {
 template <int D, bool FP8, int RW, int KW, int NK, Cap CAP>
 __global__ void __launch_bounds__(64 * RW * KW)
 __attribute__((amdgpu_waves_per_eu(RW == 4 || KW == 8 ? 2 : 1, RW == 4 || KW == 8 ? 2 : 1))) attention_kernel(
-    const AttnArgs a, const int TB, const int parts_max, const bool whole, const int desc_tiles,
+    const AttnArgs a, const int TB, const int parts_max, const Share share, const int desc_tiles,
     float* __restrict__ partials, PartDesc* __restrict__ descs) {
   using C = Attn<D, FP8, RW, KW, NK, CAP>;
   constexpr int kThreads = 64 * C::kWaves;
   extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
   __shared__ long scan_sum[C::kWaves];
+  __shared__ int scan_max[C::kWaves];
   __shared__ long found_rem;
   __shared__ int found_s;
   __shared__ SeqTiles found_seq;
@@ -252,45 +260,80 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 || KW == 8 ? 2 : 1, RW == 4 || KW == 
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int rw = wave % RW, kw = wave / RW;
   const int half = lane >> 5, col = lane & 31;
-  const int fixed = whole ? -1 : C::kSegCost;
+  bool whole = share == kWholeSegments;
   // -------- which part of the line of segments is this workgroup's
   // Up to 64 sequences: one per lane, in every wave by itself. More: a stretch of them per thread, and
   // two barriers.
   const bool few = a.S <= 64;
   const int per = few ? 1 : (a.S + kThreads - 1) / kThreads, place = few ? lane : tid;
   const int s_lo = min(place * per, a.S), s_hi = min(s_lo + per, a.S);
-  long mine = 0;
+  long mine = 0, segments = 0;   // this place's stretch of the line, and its segments
+  int longest = 0;
   SeqTiles own{};
   for (int s = s_lo; s < s_hi; ++s) {
     own = seq_tiles(a, s, TB);
-    mine += own.cost(own.MT, TB, fixed) * a.Hkv;
-  }
-  long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const long o = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += o;
-  }
-  long total = read_lane(incl, 63), before = incl - mine;
-  if (!few) {
-    if (lane == 0) scan_sum[wave] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < C::kWaves; ++i) {
-      if (i < wave) before += scan_sum[i];
-      total += scan_sum[i];
+    mine += own.cost(own.MT, TB, whole ? -1 : C::kSegCost) * a.Hkv;
+    if (share == kByLengths && own.MT > 0) {
+      segments += (long)own.MT * a.Hkv;
+      longest = max(longest, own.vis(own.MT - 1, TB) + C::kSegCost);   // the last tile sees the most
     }
-    total = uni(total);
   }
-  const int parts = (int)min((long)parts_max, whole ? total : (total + C::kMinPart - 1) / C::kMinPart);
+  // the line's length, and what lies before this place
+  long total, before;
+  auto scan = [&]() {
+    long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const long o = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += o;
+    }
+    total = read_lane(incl, 63), before = incl - mine;
+    if (!few) {
+      if (lane == 0) scan_sum[wave] = total;
+      __syncthreads();
+      total = 0;
+#pragma unroll
+      for (int i = 0; i < C::kWaves; ++i) {
+        if (i < wave) before += scan_sum[i];
+        total += scan_sum[i];
+      }
+      total = uni(total);
+    }
+  };
+  scan();
+  constexpr int kPartsMost = parts_of(C::M);
+  if constexpr (KW == 1) {
+    // Whole where no segment is longer than 5/8 of an equal part: a workgroup that takes such a one last is no more than
+    // that behind. Whole and split by the longest's share of a part: 0.29 453 and 484 us (4096 tokens of 96 heads), 0.55 160
+    // and 178 (200 prompts of 10 tokens behind up to 1400), 0.61 840 and 865 (one of 16384 tokens), 0.67 530 and 499 (2048
+    // tokens of 96 heads beside 64 sequences of 8192), 0.89 1197 and 849 (16384 tokens behind one sequence of 24000).
+    if (share == kByLengths) {
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) longest = max(longest, __shfl_xor(longest, d, 64));
+      if (!few) {
+        if (lane == 0) scan_max[wave] = longest;
+        __syncthreads();   // (scan_sum has been read as well)
+#pragma unroll
+        for (int i = 0; i < C::kWaves; ++i) longest = max(longest, scan_max[i]);
+      }
+      whole = 8l * uni(longest) * kPartsMost <= 5 * total;
+      if (whole) {
+        mine = segments;
+        scan();
+      }
+    }
+  }
+  const int fixed = whole ? -1 : C::kSegCost;
+  const int parts_split = share == kByLengths ? kPartsMost : parts_max;
+  const int parts = whole ? (int)min((long)parts_max, total)
+                          : (int)min((long)parts_split, (total + C::kMinPart - 1) / C::kMinPart);
   // Split: consecutive parts on one XCD (they walk neighbouring keys), however many there are on all
   // XCDs alike. Whole: the last tiles of a sequence, which see the most keys, first.
   const int w = whole ? parts_max - 1 - (int)blockIdx.x : xcd_tile((int)blockIdx.x, parts);
-  if (!whole && desc_tiles == 0) {   // no segment begins in these parts until one is written below
+  if (share != kWholeSegments && desc_tiles == 0) {   // no segment begins in these parts until one is written below
     if (blockIdx.x == 0)
-      for (int i = parts + tid; i < parts_max; i += kThreads) descs[i] = PartDesc{0, 0, 0, 0, 0};
-    if (w >= 0 && tid == 0) descs[w] = PartDesc{0, 0, 0, 0, 0};
+      for (int i = (whole ? 0 : parts) + tid; i < parts_split; i += kThreads) descs[i] = PartDesc{0, 0, 0, 0, 0};
+    if (!whole && w >= 0 && tid == 0) descs[w] = PartDesc{0, 0, 0, 0, 0};
   }
   if (w < 0 || w >= parts) return;
   const Parts split(total, parts);
@@ -927,7 +970,6 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 // prompt of 1500 tokens, D = 256), 450 29.8 and 31.7 (trees of 64 tokens), 512 46 and 55 (trees of 20 tokens,
 // D = 256), 1125 41 and 42 (trees of 16 tokens, e4m3), 2048 67 and 60 (trees of 5 tokens, 96 heads), 3280 101 and 85
 // (one prompt of 4096 tokens).
-constexpr int parts_of(int M) { return M == 128 ? 512 : 256; }
 static int parts_for(int M, long segments, long keys) {
   return M == 128 && segments * keys < 512l * 1024 ? 256 : parts_of(M);
 }
@@ -937,10 +979,14 @@ static int parts_for(int M, long segments, long keys) {
 // measured, shared tiles: 1639 segments of one 16384-token prompt 868 and 1007 us; about 500 of up to
 // 1024 keys 37 and 54; 100 of up to 250 keys 15 and 22; 409 of up to 4096 keys 98 and 92. A wave's own
 // keys: 256 sequences of up to 1000 keys 21 and 30; 3 of up to 200 13 and 15; one of 777 19 and 15.
-static bool take_whole(bool shared_tiles, long segments, long keys) {
-  if (keys <= 512) return true;
-  if (!shared_tiles) return segments >= 128 && keys <= 1024;
-  return segments >= 1536 || (segments >= 256 && keys <= 2048);
+// Where a table of more than 4096 keys may hold a long segment among many, the kernel looks (2048 tokens of 96
+// heads with one sequence of 131072 cached tokens: split 254 us, whole 2589; the two alone 158 and 89).
+static Share share_for(bool shared_tiles, long segments, long keys) {
+  if (keys <= 512) return kWholeSegments;
+  if (!shared_tiles) return segments >= 128 && keys <= 1024 ? kWholeSegments : kEqualParts;
+  if (segments >= 256 && keys <= 2048) return kWholeSegments;
+  if (segments >= 1536) return keys <= 4096 ? kWholeSegments : kByLengths;
+  return kEqualParts;
 }
 
 // Rows of a workgroup's tile for calls of at most max_q tokens per sequence: 32 with a wave's own
@@ -969,20 +1015,16 @@ static hipError_t launch_one(const AttnArgs& a, hipStream_t stream) {
   const long bound = (long)a.Hkv * ((a.T + TB - 1) / TB + a.S);
   const long keys = (long)a.max_pages << a.page_shift;
   // (every workgroup reads every sequence's lengths: not for thousands of sequences)
-  if (take_whole(KW == 1, segments, keys) && bound <= 1l << 22 && a.S <= 4096) {
-    const int grid = (int)bound;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, true, 0, partials,
-                       descs);
-    return hipGetLastError();
-  }
+  const Share share = bound <= 1l << 22 && a.S <= 4096 ? share_for(KW == 1, segments, keys) : kEqualParts;
   const int tiles = (a.max_q + TB - 1) / TB;
   const long most = (long)a.S * a.Hkv * tiles;   // segments, if every sequence had max_q tokens
-  const int parts = parts_for(C::M, min(most, bound), keys);
-  const bool by_segment = most <= 2 * kParts;
-  hipLaunchKernelGGL(kernel, dim3(parts), dim3(64 * C::kWaves), C::LDS, stream, a, TB, parts, false,
+  const bool by_segment = share == kEqualParts && most <= 2 * kParts;
+  const int parts = share == kEqualParts ? parts_for(C::M, min(most, bound), keys) : kParts;
+  const int grid = share == kEqualParts ? parts : (int)bound;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * C::kWaves), C::LDS, stream, a, TB, grid, share,
                      by_segment ? tiles : 0, partials, descs);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || share == kWholeSegments) return e;
   // about as many workgroups as are resident at once, and no more than a segment has rows
   const int rows = (int)min((long)C::M, (long)a.max_q * a.G);
   const int y = by_segment ? max(1, min((int)(2048 / most), min(rows, 32))) : 4;

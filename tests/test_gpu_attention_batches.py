@@ -93,3 +93,65 @@ def test_keys_and_values_apart_and_shared_pages(fp8, which):
     see = oracle.visible_tree if which == "tree" else oracle.visible_prefill
     check_rows(c, bits_of(d.out), d.lse.cpu().numpy(), [see(n, x, None if which == "tree" else 0) for x in kvs],
                128 ** -0.5, 0.0)
+
+
+def attention_time(ns, kvs, Hq, Hkv, D, page, width):
+    """Microseconds of one prefill call on random bits, the least of seven; a table of `width` tokens."""
+    pages = sum(-(-k // page) for k in kvs)
+    kv = torch.randn((pages, 2, Hkv, page, D), dtype=torch.bfloat16, device=DEV)
+    table, at = torch.zeros((len(ns), width // page), dtype=torch.int32, device=DEV), 0
+    for s, k in enumerate(kvs):
+        n = -(-k // page)
+        table[s, :n] = torch.arange(at, at + n, device=DEV)
+        at += n
+    T = sum(ns)
+    q = torch.randn((T, Hq, D), dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    cu, lens = up(np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)), up(np.array(kvs, np.int32))
+    n = L.moe_attention_workspace_bytes(len(ns), T, max(ns), Hq, Hkv, D)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    best = 1e30
+    for _ in range(7):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        L.moe_prefill_attention(q, Hq * D, kv[:, 0], kv[:, 1], L.KV_BF16, None, None, pages, page, kv.stride(0), table,
+                                table.shape[1], cu, lens, None, len(ns), T, max(ns), Hq, Hkv, D, D ** -0.5, 0.0, out, None,
+                                ws, n)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+def test_a_long_sequence_does_not_hold_up_a_chunk():
+    """A prompt's chunk with one decoding sequence of 131072 cached tokens takes about as long as the two alone, wherever
+    in the batch it stands: its keys are shared out, not walked by one workgroup (10 times the sum)."""
+    heads, width = (96, 8, 128, 64), 131072
+    alone = attention_time([2048], [2048], *heads, width) + attention_time([1], [131072], *heads, width)
+    for ns, kvs in (([1, 2048], [131072, 2048]), ([2048, 1], [2048, 131072])):
+        both = attention_time(ns, kvs, *heads, width)
+        note(f"chunk of 2048 and one of 131072: {both:.0f} us together, {alone:.0f} alone")
+        assert both < 2 * alone
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ns,kvs", [
+    ([1950], [1950]),                                                 # alike: whole segments
+    ([1950, 1], [1950, 9000]),                                        # one long one: equal parts
+    ([25] * 80, [25] * 79 + [7000]),                                  # more sequences than a wavefront has lanes, either way
+    ([25] * 80, [25 + i for i in range(80)]),
+    ([0] * 70 + [1950], [5] * 70 + [1950]),
+])
+def test_many_segments_under_a_wide_table(ns, kvs, fp8):
+    """Over 1536 row tiles by the rows of q: the lengths, not the table's width, decide how they are shared out."""
+    c = make_case(ns, kvs, 96, 8, 64, 64, fp8, seed=len(ns), lead=1, tail=2)
+    assert 8 * (c.T // (128 // 12)) >= 1536
+    see = [oracle.visible_prefill(n, k, 0) for n, k in zip(ns, kvs)]
+    run_check(c, "prefill", None, see, wide=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_padded_rows_are_no_segments(fp8):
+    """A q of many rows behind the last sequence (a captured step's padding): few segments, shared out by their lengths."""
+    c = make_case([40, 3, 1], [400, 3, 9000], 96, 8, 64, 64, fp8, seed=2, tail=2000)
+    run_check(c, "prefill", None, [oracle.visible_prefill(n, k, 0) for n, k in zip(c.ns, c.kvs)], wide=True)
