@@ -412,7 +412,8 @@ int moe_kv_append(const uint16_t* qkv, size_t qkv_stride, int T, int num_q_heads
  *   limits: those of the cache; num_q_heads a multiple of num_kv_heads, at most 128 times
  *   it, num_q_heads <= 1024; S <= 65536; max_pages * page_size < 2^30; 0 < scale <= 1e6;
  *   softcap 0 or in 1e-6..1e6. out and lse overlap no input.
- * Results do not depend on scheduling: no atomics, sums in a fixed order. */
+ * Results do not depend on scheduling: no atomics, sums in a fixed order. That order goes by the call's sizes (S, T,
+ * max_q, max_pages * page_size) and its sequences' lengths, so a sequence's last bits may differ between batches. */
 int moe_tree_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
                        const float* k_scale, const float* v_scale, int num_pages, int page_size,
                        size_t page_stride, const int32_t* block_table, int max_pages, const int32_t* cu_q,
