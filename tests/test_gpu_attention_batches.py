@@ -155,3 +155,45 @@ def test_padded_rows_are_no_segments(fp8):
     """A q of many rows behind the last sequence (a captured step's padding): few segments, shared out by their lengths."""
     c = make_case([40, 3, 1], [400, 3, 9000], 96, 8, 64, 64, fp8, seed=2, tail=2000)
     run_check(c, "prefill", None, [oracle.visible_prefill(n, k, 0) for n, k in zip(c.ns, c.kvs)], wide=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_replays_that_change_how_segments_are_shared_out(fp8):
+    """Captured once; lengths that make whole segments and lengths that make equal parts take turns, with eager calls between:
+    each replay's bits are the eager call's, and nothing of the turn before is left in the workspace."""
+    ns, page = [1950, 1], 64
+    cases = []
+    for kvs in ([1950, 20000], [1950, 300], [2400, 9000], [1960, 1]):
+        used = sum(-(-k // page) for k in kvs)
+        c = make_case(ns, kvs, 96, 8, 64, page, fp8, seed=kvs[1], extra_pages=360 - used)
+        t = np.zeros((2, 400), np.int32)
+        t[:, :c.table.shape[1]] = np.where(c.table == 1 << 30, 0, c.table)
+        c.table = t
+        cases.append(c)
+    devs = [Dev(c) for c in cases]
+    eager = []
+    for d in devs:
+        d.call("prefill")
+        torch.cuda.synchronize()
+        eager.append((bits_of(d.out).copy(), d.lse.cpu().numpy().copy()))
+    # one of each kind against the oracle, the others against these by their bits
+    for i in (0, 1):
+        check_rows(cases[i], *eager[i], [oracle.visible_prefill(n, k, 0) for n, k in zip(ns, cases[i].kvs)], 64 ** -0.5, 0.0)
+    g, stream, graph = Dev(cases[1]), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    note(f"replays between whole segments and equal parts fp8={fp8}")
+    with torch.cuda.stream(stream):
+        g.call("prefill", stream=stream)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            g.call("prefill", stream=stream)
+    for i in (0, 1, 2, 3, 1, 0, 3, 2):
+        for name in ("q", "kv", "table", "cu", "kvl", "ks", "vs"):
+            getattr(g, name).copy_(getattr(devs[i], name))
+        g.out.fill_(0x7FC1)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(bits_of(g.out), eager[i][0]) and np.array_equal(g.lse.cpu().numpy(), eager[i][1]), i
+        devs[i].call("prefill")
+        torch.cuda.synchronize()
+        assert np.array_equal(bits_of(devs[i].out), eager[i][0])
