@@ -426,7 +426,20 @@ int moe_prefill_attention(const uint16_t* q, size_t q_stride, const void* k_cach
                           const int32_t* kv_lens, const int32_t* prefix_lens, int S, int T, int max_q,
                           int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap,
                           uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
-/* Bytes of workspace for either call (host; 0 for sizes that they refuse). */
+/* moe_window_attention: moe_prefill_attention's causal chunks (max_q 1: one token per sequence, decoding) with a sliding
+ * window and sinks. Token i sees the cached tokens j <= p = ctx + i with j > p - window (its own included: window tokens
+ * at most) or j < sinks. window >= 1, sinks >= 0; other arguments, workspace and rounding as above.
+ * A cached token that none of its sequence's query tokens sees is not used, whatever the cache holds there, and of
+ * block_table only the entries of pages that hold a token seen are read: pages that the window has left may be given
+ * to others, their entries may hold anything. The keys walked are those of the sinks and the windows, so a call's time does not
+ * grow with kv_lens. */
+int moe_window_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
+                         const float* k_scale, const float* v_scale, int num_pages, int page_size, size_t page_stride,
+                         const int32_t* block_table, int max_pages, const int32_t* cu_q, const int32_t* kv_lens,
+                         int window, int sinks, int S, int T, int max_q, int num_q_heads, int num_kv_heads,
+                         int head_dim, float scale, float softcap, uint16_t* out, float* lse, void* workspace,
+                         size_t ws_bytes, void* stream);
+/* Bytes of workspace for any of the three calls (host; 0 for sizes that they refuse). */
 size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim);
 
 /* Host helpers. */

@@ -36,6 +36,13 @@ def visible_prefill(n: int, kv: int, prefix: int) -> np.ndarray:
     return (j <= kv - n + i) | (j < prefix)
 
 
+def visible_window(n: int, kv: int, window: int, sinks: int) -> np.ndarray:
+    """[n, kv] booleans: token j for row i, at position p = kv - n + i, when j <= p and (p - j < window or j < sinks)."""
+    j = np.arange(max(kv, 0))[None, :]
+    p = kv - n + np.arange(n)[:, None]
+    return (j <= p) & ((p - j < window) | (j < sinks))
+
+
 def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, see: np.ndarray, scale: float, softcap: float = 0.0):
     """One sequence: q [n, Hq, D], k and v [kv, Hkv, D], see [n, kv] -> out [n, Hq, D], lse [n, Hq],
     and for error bounds the weighted mean of |v| [n, Hq, D] and the largest sum |q_d k_d| * scale [n, Hq]."""

@@ -63,6 +63,7 @@ def _load():
         "moe_tree_attention": ([P, Z, P, P, I, P, P, I, I, Z, P, I, P, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P], I),
         "moe_prefill_attention": ([P, Z, P, P, I, P, P, I, I, Z, P, I, P, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P],
                                   I),
+        "moe_window_attention": ([P, Z, P, P, I, P, P, I, I, Z, P, I, P, P, I, I, I, I, I, I, I, I, F, F, P, P, P, Z, P], I),
         "moe_attention_workspace_bytes": ([I, I, I, I, I, I], Z),
         "moe_rope_cos_sin_table": ([P, I, I, ctypes.c_double, P], I),
         "moe_sorted_capacity": ([I, I, I, I], Z),
@@ -95,7 +96,7 @@ EXPORTED = ("moe_route_topk_plus_shared", "moe_align_by_expert", "moe_fused_ffn"
             "moe_align_workspace_bytes", "moe_ffn_workspace_bytes", "moe_ffn_workspace_offsets",
             "srmoe_status_string", "srmoe_last_hip_error", "moe_workspace_bytes", "moe_status_string",
             "moe_layer_forward_staged", "moe_layer_forward_noalloc", "srmoe_source_hash", "moe_kv_append",
-            "moe_tree_attention", "moe_prefill_attention", "moe_attention_workspace_bytes")
+            "moe_tree_attention", "moe_prefill_attention", "moe_attention_workspace_bytes", "moe_window_attention")
 
 
 def _ptr(t):
@@ -349,3 +350,13 @@ def moe_prefill_attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_sca
                                    num_kv_heads, head_dim, scale, softcap, _ptr(out), _ptr(lse), _ptr(workspace),
                                    ws_bytes, _stream(stream))
     return _check("moe_prefill_attention", st) if check else st
+
+
+def moe_window_attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
+                         block_table, max_pages, cu_q, kv_lens, window, sinks, S, T, max_q, num_q_heads, num_kv_heads,
+                         head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream=None, check=True):
+    st = lib.moe_window_attention(_ptr(q), q_stride, _ptr(k_cache), _ptr(v_cache), kv_type, _ptr(k_scale), _ptr(v_scale),
+                                  num_pages, page_size, page_stride, _ptr(block_table), max_pages, _ptr(cu_q),
+                                  _ptr(kv_lens), window, sinks, S, T, max_q, num_q_heads, num_kv_heads, head_dim, scale,
+                                  softcap, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
+    return _check("moe_window_attention", st) if check else st

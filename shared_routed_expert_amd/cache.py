@@ -1,7 +1,7 @@
 """A paged key/value cache on the GPU and the calls that write and read it.
 
 Torch provides device memory and the stream (always torch's current stream of the cache's device); the
-writes (moe_kv_append) and the attention (moe_tree_attention, moe_prefill_attention) run in
+writes (moe_kv_append) and the attention (moe_tree_attention, moe_prefill_attention, moe_window_attention) run in
 libsrmoe.so's HIP kernels. Every tensor starts on a 16-byte boundary, as torch allocates them; a slice that does not is
 refused by name.
 """
@@ -121,7 +121,7 @@ class PagedKVCache:
         # from torch's allocator for each call: stream-ordered, and a captured graph keeps its own
         ws = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
         self._run(call, q, q.stride(0) if T > 1 else Hq * D, self.k, self.v, self.kv_type, self.k_scale, self.v_scale,
-                  self.num_pages, self.page_size, self.kv.stride(0), block_table, max_pages, cu_q, kv_lens, extra, S, T,
+                  self.num_pages, self.page_size, self.kv.stride(0), block_table, max_pages, cu_q, kv_lens, *extra, S, T,
                   max_q, Hq, self.num_kv_heads, D, D ** -0.5 if scale is None else scale, softcap, out, lse, ws, n)
         return out
 
@@ -133,8 +133,8 @@ class PagedKVCache:
         sequence's tokens past max_q are zero, or left as they were in an out (and lse) that is given."""
         if tree_mask is not None:
             self._tensor(tree_mask, "tree_mask", torch.int64, (q.shape[0],))
-        return self._attention(L.moe_tree_attention, q, block_table, cu_q, kv_lens, tree_mask, max_q, scale, softcap, out,
-                               lse)
+        return self._attention(L.moe_tree_attention, q, block_table, cu_q, kv_lens, (tree_mask,), max_q, scale, softcap,
+                               out, lse)
 
     def prefill_attention(self, q, block_table, cu_q, kv_lens, max_q, prefix_lens=None, scale=None, softcap=0.0, out=None,
                           lse=None):
@@ -143,5 +143,16 @@ class PagedKVCache:
         outside every sequence as in tree_attention."""
         if prefix_lens is not None:
             self._tensor(prefix_lens, "prefix_lens", torch.int32, (block_table.shape[0],))
-        return self._attention(L.moe_prefill_attention, q, block_table, cu_q, kv_lens, prefix_lens, max_q, scale, softcap,
-                               out, lse)
+        return self._attention(L.moe_prefill_attention, q, block_table, cu_q, kv_lens, (prefix_lens,), max_q, scale,
+                               softcap, out, lse)
+
+    def window_attention(self, q, block_table, cu_q, kv_lens, max_q, window, sinks=0, scale=None, softcap=0.0, out=None,
+                         lse=None):
+        """Causal attention of a chunk's tokens (max_q 1: decoding), each over the last `window` cached tokens up to
+        itself and the sequence's first `sinks`. Tokens that nobody sees are not used and their pages' entries in
+        block_table may hold anything: pages that the window has left may be given to others. scale, out, lse and the rows
+        outside every sequence as in tree_attention."""
+        _need(isinstance(window, int) and isinstance(sinks, int) and 1 <= window < 2 ** 31 and 0 <= sinks < 2 ** 31,
+              "window is a whole number of at least 1, sinks of at least 0")
+        return self._attention(L.moe_window_attention, q, block_table, cu_q, kv_lens, (window, sinks), max_q, scale,
+                               softcap, out, lse)

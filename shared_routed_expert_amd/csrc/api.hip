@@ -815,9 +815,9 @@ size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, i
 static int attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
                      const float* k_scale, const float* v_scale, int num_pages, int page_size, size_t page_stride,
                      const int32_t* block_table, int max_pages, const int32_t* cu_q, const int32_t* kv_lens,
-                     const uint64_t* tree_mask, const int32_t* prefix_lens, int S, int T, int max_q,
+                     const uint64_t* tree_mask, const int32_t* prefix_lens, int window, int sinks, int S, int T, int max_q,
                      int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap, uint16_t* out,
-                     float* lse, void* workspace, size_t ws_bytes, void* stream) {
+                     float* lse, void* workspace, size_t ws_bytes, void* stream) {   // window 0: none
   int st = check_attention_dims(S, T, max_q, num_q_heads, num_kv_heads, head_dim);
   if (st != SRMOE_OK) return st;
   st = check_cache_dims(kv_type, num_kv_heads, head_dim, num_pages, page_size, page_stride);
@@ -846,8 +846,8 @@ static int attention(const uint16_t* q, size_t q_stride, const void* k_cache, co
   a.block_table = block_table; a.max_pages = max_pages; a.cu_q = cu_q; a.kv_lens = kv_lens;
   a.tree_mask = tree_mask; a.prefix_lens = prefix_lens; a.S = S; a.T = T; a.max_q = max_q; a.Hq = num_q_heads;
   a.Hkv = num_kv_heads; a.G = num_q_heads / num_kv_heads; a.D = head_dim; a.scale = scale; a.softcap = softcap;
-  a.out = out; a.lse = lse; a.ws = workspace;
-  return hip_status(launch_attention(a, as_stream(stream)));
+  a.out = out; a.lse = lse; a.ws = workspace; a.window = window; a.sinks = sinks;
+  return hip_status(window ? launch_window_attention(a, as_stream(stream)) : launch_attention(a, as_stream(stream)));
 }
 
 int moe_tree_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
@@ -858,8 +858,8 @@ int moe_tree_attention(const uint16_t* q, size_t q_stride, const void* k_cache, 
                        float* lse, void* workspace, size_t ws_bytes, void* stream) {
   if (max_q > 64) return SRMOE_ERR_UNSUPPORTED;   // a token's mask is one 64-bit word
   return attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
-                   block_table, max_pages, cu_q, kv_lens, tree_mask, nullptr, S, T, max_q, num_q_heads,
-                   num_kv_heads, head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream);
+                   block_table, max_pages, cu_q, kv_lens, tree_mask, nullptr, 0, 0, S, T, max_q, num_q_heads, num_kv_heads,
+                   head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream);
 }
 
 int moe_prefill_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
@@ -869,7 +869,22 @@ int moe_prefill_attention(const uint16_t* q, size_t q_stride, const void* k_cach
                           int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap,
                           uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
   return attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
-                   block_table, max_pages, cu_q, kv_lens, nullptr, prefix_lens, S, T, max_q, num_q_heads,
+                   block_table, max_pages, cu_q, kv_lens, nullptr, prefix_lens, 0, 0, S, T, max_q, num_q_heads, num_kv_heads,
+                   head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream);
+}
+
+int moe_window_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
+                         const float* k_scale, const float* v_scale, int num_pages, int page_size, size_t page_stride,
+                         const int32_t* block_table, int max_pages, const int32_t* cu_q, const int32_t* kv_lens,
+                         int window, int sinks, int S, int T, int max_q, int num_q_heads, int num_kv_heads,
+                         int head_dim, float scale, float softcap, uint16_t* out, float* lse, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return SRMOE_ERR_INVALID_ARG;
+  // (tokens are numbered below 2^30: more of either is all of them)
+  window = window < (1 << 30) ? window : 1 << 30;
+  sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+  return attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
+                   block_table, max_pages, cu_q, kv_lens, nullptr, nullptr, window, sinks, S, T, max_q, num_q_heads,
                    num_kv_heads, head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream);
 }
 

@@ -36,6 +36,7 @@ struct AttnArgs {
   const int32_t *cu_q, *kv_lens;
   const uint64_t* tree_mask;        // null: causal
   const int32_t* prefix_lens;       // null: no prefix
+  int window, sinks;                // read by launch_window_attention alone
   int S, T, max_q, Hq, Hkv, G, D;
   float scale, softcap;
   uint16_t* out;
@@ -44,6 +45,7 @@ struct AttnArgs {
 };
 
 hipError_t launch_attention(const AttnArgs&, hipStream_t);
+hipError_t launch_window_attention(const AttnArgs&, hipStream_t);
 size_t attention_workspace_bytes(int S, int max_q, int Hq, int Hkv, int D);
 
 // One sequence of an attention call, with every length taken from device memory held to
