@@ -336,6 +336,27 @@ int moe_qk_norm_rope(uint16_t* qkv, int T, int num_q_heads, int num_kv_heads, in
 int moe_rope_cos_sin_table(float* cos_sin, int max_pos, int rotary_dim, double theta, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The norm between the attention and the layer: per token t
+ *     h = x[t] + residual[t] (float32)        residual_out[t] = bf16(h)
+ *     y = h / sqrt(mean(h^2) + eps) * weight (float32)
+ * and y as bf16 (what the router reads) and/or as e4m3 codes with scales (what the expert GEMMs read):
+ *     sx = max |y| / 448 (1 where that is 0), xq = e4m3(y / sx), to nearest even, over the row
+ *     (SRMOE_SCALE_PER_CHANNEL: sx [T]) or over each 128 columns (SRMOE_SCALE_BLOCK128: sx [T, H / 128]).
+ * xq and sx have the layout of moe_ffn_workspace_offsets' x_q and x scales: written there they take the place of
+ * moe_ffn_quant_x ahead of moe_ffn_experts, or of moe_ffn_gate_up + moe_ffn_down, one pass over x and one rounding to
+ * bf16 fewer (the codes are of y itself, not of its bf16 value).
+ *   x            rows of H bf16 values, x_stride values apart (>= H, a multiple of 8)
+ *   residual     [T,H] bf16, or NULL: none (h = x);  residual_out [T,H] bf16, or NULL. It may be residual itself.
+ *   weight       [H] float32;  y [T,H] bf16, or NULL (it may be x where x_stride == H)
+ *   xq           [T,H] e4m3, or NULL (then sx is NULL and scale_mode is not used): y or xq is given
+ * No other output overlaps an input. Sums and scales are float32 (h^2 up to 2^127); a NaN or an infinity stays in its row.
+ *   limits: H % 8 == 0 (block scales: H % 128 == 0), H <= 65536, 0 <= eps < 1e30.
+ * ------------------------------------------------------------------------- */
+int moe_add_rms_norm(const uint16_t* x, size_t x_stride, const uint16_t* residual, uint16_t* residual_out,
+                     const float* weight, float eps, int T, int H, int scale_mode, uint16_t* y, uint8_t* xq, float* sx,
+                     void* stream);
+
+/* ---------------------------------------------------------------------------
  * The paged key/value cache behind that step, and the attention that reads it.
  *
  * Cache: k_cache and v_cache are arrays of num_pages pages, page_stride ELEMENTS apart

@@ -43,3 +43,4 @@ __all__ = ["qk_norm_rope", "head_rms_norm", "rope_half", "rope_interleaved", "ro
            "expert_ffn", "moe_unfused", "moe_fused", "slot_outputs", "combine_slots",
            "dense_shared_ffn"]
 from .kv import attend, visible_tree, visible_prefill, visible_window
+from .norm import add_rms_norm, act_scales

@@ -65,6 +65,7 @@ def _load():
                                   I),
         "moe_window_attention": ([P, Z, P, P, I, P, P, I, I, Z, P, I, P, P, I, I, I, I, I, I, I, I, F, F, P, P, P, Z, P], I),
         "moe_attention_workspace_bytes": ([I, I, I, I, I, I], Z),
+        "moe_add_rms_norm": ([P, Z, P, P, P, F, I, I, I, P, P, P, P], I),
         "moe_rope_cos_sin_table": ([P, I, I, ctypes.c_double, P], I),
         "moe_sorted_capacity": ([I, I, I, I], Z),
         "moe_align_workspace_bytes": ([I, I, I], Z),
@@ -96,7 +97,8 @@ EXPORTED = ("moe_route_topk_plus_shared", "moe_align_by_expert", "moe_fused_ffn"
             "moe_align_workspace_bytes", "moe_ffn_workspace_bytes", "moe_ffn_workspace_offsets",
             "srmoe_status_string", "srmoe_last_hip_error", "moe_workspace_bytes", "moe_status_string",
             "moe_layer_forward_staged", "moe_layer_forward_noalloc", "srmoe_source_hash", "moe_kv_append",
-            "moe_tree_attention", "moe_prefill_attention", "moe_attention_workspace_bytes", "moe_window_attention")
+            "moe_tree_attention", "moe_prefill_attention", "moe_attention_workspace_bytes", "moe_window_attention",
+            "moe_add_rms_norm")
 
 
 def _ptr(t):
@@ -292,6 +294,13 @@ def moe_qk_norm_rope(qkv, T, num_q_heads, num_kv_heads, head_dim, rotary_dim, ne
 def moe_rope_cos_sin_table(cos_sin, max_pos, rotary_dim, theta, stream=None, check=True):
     st = lib.moe_rope_cos_sin_table(_ptr(cos_sin), max_pos, rotary_dim, float(theta), _stream(stream))
     return _check("moe_rope_cos_sin_table", st) if check else st
+
+
+def moe_add_rms_norm(x, x_stride, residual, residual_out, weight, eps, T, H, scale_mode, y, xq, sx, stream=None,
+                     check=True):
+    st = lib.moe_add_rms_norm(_ptr(x), x_stride, _ptr(residual), _ptr(residual_out), _ptr(weight), eps, T, H, scale_mode,
+                              _ptr(y), _ptr(xq), _ptr(sx), _stream(stream))
+    return _check("moe_add_rms_norm", st) if check else st
 
 
 def moe_route_from_x_workspace_bytes(T, H, E):

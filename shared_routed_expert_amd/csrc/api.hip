@@ -7,6 +7,7 @@
 
 #include "attention.hpp"
 #include "front_dev.hpp"
+#include "norm.hpp"
 
 namespace srmoe {
 hipError_t launch_route(const LogitSrc&, int, int, int, float, int32_t*, float*, hipStream_t);
@@ -741,6 +742,25 @@ int moe_qk_norm_rope(uint16_t* qkv, int T, int num_q_heads, int num_kv_heads, in
   return hip_status(launch_qk_norm_rope(qkv, T, num_q_heads, num_kv_heads, head_dim, rotary_dim, neox != 0,
                                         q_norm_w, k_norm_w, eps, positions, cos_sin, max_pos, fused != 0,
                                         as_stream(stream)));
+}
+
+int moe_add_rms_norm(const uint16_t* x, size_t x_stride, const uint16_t* residual, uint16_t* residual_out,
+                     const float* weight, float eps, int T, int H, int scale_mode, uint16_t* y, uint8_t* xq, float* sx,
+                     void* stream) {
+  if (T < 0 || T > kMaxT || H <= 0 || !(eps >= 0.f) || !(eps < 1e30f)) return SRMOE_ERR_INVALID_ARG;
+  if (scale_mode != SRMOE_SCALE_PER_CHANNEL && scale_mode != SRMOE_SCALE_BLOCK128) return SRMOE_ERR_INVALID_ARG;
+  if (H % 8 != 0 || H > 65536 || (xq && scale_mode == SRMOE_SCALE_BLOCK128 && H % kGroup != 0))
+    return SRMOE_ERR_UNSUPPORTED;
+  if (x_stride < (size_t)H || x_stride % 8 != 0 || x_stride >= ((size_t)1 << 40)) return SRMOE_ERR_INVALID_ARG;
+  if (T == 0) return SRMOE_OK;
+  if (!x || !weight || (!y && !xq) || (xq != nullptr) != (sx != nullptr)) return SRMOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, residual, residual_out, weight, y, xq, sx};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
+  NormArgs a{};
+  a.x = x; a.x_stride = x_stride; a.residual = residual; a.residual_out = residual_out; a.weight = weight; a.eps = eps;
+  a.T = T; a.H = H; a.block = scale_mode == SRMOE_SCALE_BLOCK128; a.y = y; a.xq = xq; a.sx = sx;
+  return hip_status(launch_add_rms_norm(a, as_stream(stream)));
 }
 
 // ---------------------------------------------------------------------------------------

@@ -133,19 +133,65 @@ class FusedMoE:
                                           self.expert_offsets, self.num_padded, self.align_ws, self.align_ws_bytes,
                                           self.ws, self.ws_bytes, self.out, list(events), stream)
 
+    def _router_ws(self):
+        if not hasattr(self, "router_ws"):
+            self.router_ws_bytes = L.moe_route_from_x_workspace_bytes(self.T, self.H, self.E)
+            self.router_ws = torch.empty(max(self.router_ws_bytes, 16), dtype=torch.uint8, device=self.out.device)
+
     def forward_from_x(self, x, w_router, bias, W: DeviceWeights, shared_weight=1.0, stream=None):
         """The layer from x and the router weight (moe_layer_forward_from_x: the router gate
         in front, its partial sums folded into the routing)."""
         T, H, I, E1, K1, bm = self.dims()
-        if not hasattr(self, "router_ws"):
-            self.router_ws_bytes = L.moe_route_from_x_workspace_bytes(T, H, self.E)
-            self.router_ws = torch.empty(max(self.router_ws_bytes, 16), dtype=torch.uint8, device=self.out.device)
+        self._router_ws()
         L.moe_layer_forward_from_x(x, w_router, bias, W.w13, W.s13, W.w2, W.s2, self.scale_mode, T, H, I, self.E,
                                    self.K, shared_weight, bm, self.topk_ids, self.topk_w, self.sorted_slot_ids,
                                    self.block_expert, self.expert_counts, self.expert_offsets, self.num_padded,
                                    self.router_ws, self.router_ws_bytes, self.align_ws, self.align_ws_bytes,
                                    self.ws, self.ws_bytes, self.out, stream)
         return self.out
+
+    def add_norm(self, x, weight, residual=None, eps=1e-5, residual_out=None, y=None, stream=None):
+        """moe_add_rms_norm in front of the layer: h = x + residual (x alone without one), y = its root-mean-square norm
+        times weight [H] float32. Returns (y, h) in bf16 (h: None without a residual, unless residual_out is given) and leaves
+        y's codes and scales in the workspace, where experts_normed finds them. x [T, H] bf16, rows may be
+        strided."""
+        T, H = self.T, self.H
+        for t, name in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (y, "y")):
+            if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, H) or t.device != self.out.device):
+                raise ValueError(f"{name} is bf16 [{T}, {H}] on {self.out.device}")
+            if t is not None and (t.stride(1) != 1 and H > 1 or t is not x and not t.is_contiguous()):
+                raise ValueError(f"{name} is contiguous" + (" in its rows" if t is x else ""))
+        if x is None or weight is None or weight.dtype != torch.float32 or tuple(weight.shape) != (H,) \
+                or not weight.is_contiguous() or weight.device != self.out.device:
+            raise ValueError(f"weight is float32 [{H}] on {self.out.device}")
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(residual)
+        if y is None:
+            y = torch.empty((T, H), dtype=torch.bfloat16, device=self.out.device)
+        base = self.ws.data_ptr()
+        L.moe_add_rms_norm(x, x.stride(0) if T > 1 else H, residual, residual_out, weight, eps, T, H, self.scale_mode, y,
+                           base + self.offsets["xq"], base + self.offsets["sx"], stream)
+        return y, residual_out
+
+    def experts_normed(self, W: DeviceWeights, stream=None):
+        """The experts on what add_norm left in the workspace, by the routing tables of route and align (or of
+        forward_normed): moe_fused_ffn without its quantisation of x, then the combine."""
+        T, H, I, E1, K1, bm = self.dims()
+        L.moe_ffn_experts(W.w13, W.s13, W.w2, W.s2, self.scale_mode, T, H, I, E1, K1, bm, self.sorted_slot_ids,
+                          self.block_expert, self.num_padded, self.topk_w, self.ws, self.ws_bytes, stream)
+        self.combine(stream)
+        return self.out
+
+    def forward_normed(self, x, norm_w, w_router, bias, W: DeviceWeights, residual=None, eps=1e-5, residual_out=None,
+                       shared_weight=1.0, stream=None):
+        """What stands behind the attention, whole: add_norm, the router gate and routing on y, and the layer on y's
+        codes. Returns (out, residual_out)."""
+        y, h = self.add_norm(x, norm_w, residual, eps, residual_out, stream=stream)
+        self._router_ws()
+        L.moe_route_from_x(y, w_router, bias, self.T, self.H, self.E, self.K, shared_weight, self.topk_ids, self.topk_w,
+                           self.router_ws, self.router_ws_bytes, stream)
+        self.align(stream)
+        return self.experts_normed(W, stream), h
 
     # views into the workspace, for inspecting the stages
     def ws_view(self, name, dtype, shape):
