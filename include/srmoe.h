@@ -463,6 +463,58 @@ int moe_window_attention(const uint16_t* q, size_t q_stride, const void* k_cache
 /* Bytes of workspace for any of the three calls (host; 0 for sizes that they refuse). */
 size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim);
 
+/* ---------------------------------------------------------------------------
+ * Eviction by accumulated attention weight: what the cached tokens have received, and the cut of a sequence to a budget.
+ *
+ * moe_kv_usage: per sequence s, kv head h and cached token j < kv_lens[s], with the scores z and the masks of
+ * moe_prefill_attention (max_q 1: of decoding) and its lse,
+ *     usage[row,h,j] = sum over the sequence's tokens i that see j, and the query heads g of kv head h, of
+ *                      exp(z_{i,g,j} - lse[i,g]), + decay * prev[row,h,j] for j < ctx when prev is given
+ * (the call's own tokens, j >= ctx = kv_lens[s] - n_s, begin at 0: prev is not read there, whatever it holds).
+ *   lse          [T, num_q_heads] float32, of the attention call on the same q, or of any subset of its rows with q and cu_q to
+ *                match: the last tokens of a prompt alone, say. -infinity (a row that saw nothing) adds nothing; a
+ *                NaN makes the tokens that its row sees NaN.
+ *   prev, usage  [rows, num_kv_heads, max_pages * page_size] float32; prev NULL (nothing is known of the tokens before), or
+ *                usage itself, or another array
+ *   usage_rows   [S] int32: sequence s's row of them, or NULL: row s (rows >= S). A sequence whose row is outside
+ *                [0, rows) is not kept; two sequences of one row leave it undefined.
+ *   Sequences without query tokens, rows of no sequence and tokens past kv_lens keep what usage holds. A token of a page
+ *   outside the pool gets 0 from this call. Weights and sums are float32, in a fixed order (no atomics).
+ *   workspace    >= moe_kv_usage_workspace_bytes(...); limits and other arguments as for moe_prefill_attention; 0 <=
+ *                decay <= 1. usage overlaps no input but prev.
+ *
+ * moe_kv_evict: every sequence with kv_lens[s] > limit is cut to `budget` tokens, each kv head by its own usage: it keeps
+ * the first `sinks`, the last `recent`, and of those between them the budget - sinks - recent of largest usage (equal
+ * ones: the earlier; NaN counts as lowest; a sequence whose row is outside [0, rows): all are equal). The kept tokens stay
+ * in order of position; the i-th one's key and value are copied to the i-th place of the sequence's new pages:
+ *   new_table    [S, new_max_pages] int32, new_max_pages * page_size >= budget: pages that no sequence reads in this call and
+ *                that stand nowhere else in it (they get other tokens than one expects otherwise). Of block_table
+ *                nothing changes: pages that sequences share stay whole, and the caller takes the sequence's new row and
+ *                gives the old pages back. Tokens whose new page is outside the pool are not copied; tokens of a page outside
+ *                it become zeros.
+ *   new_lens     [S] int32 out: budget, or kv_lens[s] (at most max_pages * page_size) where nothing is cut
+ *   kept         [S, num_kv_heads, budget] int32 out: the old places of the kept tokens, ascending
+ *   new_usage    as usage, out: the kept tokens' usage in their new places 0 .. budget - 1; it may be usage itself.
+ *   Rows of sequences that are not cut, in kept, new_usage and the cache, keep what they hold, as do the places past budget.
+ *   limits: those of the cache; 1 <= budget <= limit; sinks, recent >= 0, sinks + recent <= budget; S * num_kv_heads <=
+ *   65535; max_pages * page_size < 2^30. new_lens is not kv_lens, new_table not block_table.
+ * The cut leaves keys at the positions that they were rotated to; what comes next is appended behind the budget with its
+ * own position.
+ * ------------------------------------------------------------------------- */
+int moe_kv_usage(const uint16_t* q, size_t q_stride, const void* k_cache, int kv_type, const float* k_scale,
+                 int num_pages, int page_size, size_t page_stride, const int32_t* block_table, int max_pages,
+                 const int32_t* cu_q, const int32_t* kv_lens, const int32_t* prefix_lens, const float* lse, int S, int T,
+                 int max_q, int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap,
+                 const float* prev, float decay, float* usage, const int32_t* usage_rows, int rows, void* workspace,
+                 size_t ws_bytes, void* stream);
+/* Bytes of workspace (host; 0 for sizes that the call refuses). */
+size_t moe_kv_usage_workspace_bytes(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim);
+int moe_kv_evict(void* k_cache, void* v_cache, int kv_type, int num_pages, int page_size, size_t page_stride,
+                 const int32_t* block_table, int max_pages, const int32_t* kv_lens, const float* usage, float* new_usage,
+                 const int32_t* usage_rows, int rows, int S, int num_kv_heads, int head_dim, int limit, int budget,
+                 int sinks, int recent, const int32_t* new_table, int new_max_pages, int32_t* new_lens, int32_t* kept,
+                 void* stream);
+
 /* Host helpers. */
 size_t moe_sorted_capacity(int T, int K1, int E1, int block_m); /* P_max, rows */
 size_t moe_align_workspace_bytes(int T, int K1, int E1);

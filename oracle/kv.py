@@ -70,3 +70,36 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, see: np.ndarray, scale: 
         lse[:, h] = np.where(some, m + np.log(total), -np.inf)
         dot[:, h] = np.where(see, scale * (np.abs(qh) @ np.abs(kh).T), 0.0).max(axis=1)
     return out, lse, mag, dot
+
+
+def usage(q: np.ndarray, k: np.ndarray, see: np.ndarray, lse: np.ndarray, scale: float, softcap: float = 0.0):
+    """One sequence: q [n, Hq, D], k [kv, Hkv, D], see [n, kv], lse [n, Hq] -> [Hkv, kv] sums over the tokens and the heads
+    of a kv head of exp(z - lse), and for error bounds the same sums with every weight times the row's largest
+    sum |q_d k_d| * scale."""
+    n, Hq, D = q.shape
+    Hkv = k.shape[1]
+    group = Hq // Hkv
+    out, spread = np.zeros((Hkv, see.shape[1])), np.zeros((Hkv, see.shape[1]))
+    if n == 0 or see.shape[1] == 0:
+        return out, spread
+    for h in range(Hq):
+        kh, qh = np.asarray(k[:, h // group], np.float64), np.asarray(q[:, h], np.float64)
+        z = scale * (qh @ kh.T)
+        if softcap > 0:
+            z = softcap * np.tanh(z / softcap)
+        top = np.where(np.isneginf(lse[:, h]), np.inf, lse[:, h]).astype(np.float64)
+        p = np.where(see, np.exp(z - top[:, None]), 0.0)
+        dot = np.where(see, scale * (np.abs(qh) @ np.abs(kh).T), 0.0).max(axis=1)
+        out[h // group] += p.sum(axis=0)
+        spread[h // group] += (p * dot[:, None]).sum(axis=0)
+    return out, spread
+
+
+def kept_tokens(usage_row: np.ndarray, n: int, budget: int, sinks: int, recent: int) -> np.ndarray:
+    """The places, ascending, of the `budget` of n tokens that stay: the first `sinks`, the last `recent`, and of the rest
+    those of largest usage, equal ones by place; NaN below everything."""
+    middle = list(range(sinks, n - recent))
+    value = [(-np.inf, 0) if np.isnan(usage_row[j]) else (usage_row[j], 1) for j in middle]
+    best = sorted(range(len(middle)), key=lambda i: (-value[i][0], -value[i][1], middle[i]))
+    chosen = [middle[i] for i in best[:budget - sinks - recent]]
+    return np.array(sorted(list(range(sinks)) + chosen + list(range(n - recent, n))), np.int32)

@@ -16,7 +16,7 @@ _BINDING = ("lib", "LIB_PATH", "SrmoeError", "SCALE_PER_CHANNEL", "SCALE_BLOCK12
             "moe_workspace_bytes", "moe_status_string", "moe_layer_forward_staged",
             "moe_layer_forward_noalloc", "NOALLOC_SCRATCH_BYTES", "KV_BF16", "KV_E4M3", "moe_kv_append",
             "moe_tree_attention", "moe_prefill_attention", "moe_window_attention", "moe_attention_workspace_bytes",
-            "moe_add_rms_norm")
+            "moe_add_rms_norm", "moe_kv_usage", "moe_kv_usage_workspace_bytes", "moe_kv_evict")
 _LAYER = ("FusedMoE", "UnfusedMoE", "DeviceWeights")
 _CACHE = ("PagedKVCache",)
 

@@ -64,6 +64,9 @@ def _load():
         "moe_prefill_attention": ([P, Z, P, P, I, P, P, I, I, Z, P, I, P, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P],
                                   I),
         "moe_window_attention": ([P, Z, P, P, I, P, P, I, I, Z, P, I, P, P, I, I, I, I, I, I, I, I, F, F, P, P, P, Z, P], I),
+        "moe_kv_usage": ([P, Z, P, I, P, I, I, Z, P, I, P, P, P, P, I, I, I, I, I, I, F, F, P, F, P, P, I, P, Z, P], I),
+        "moe_kv_usage_workspace_bytes": ([I, I, I, I, I, I], Z),
+        "moe_kv_evict": ([P, P, I, I, I, Z, P, I, P, P, P, P, I, I, I, I, I, I, I, I, P, I, P, P, P], I),
         "moe_attention_workspace_bytes": ([I, I, I, I, I, I], Z),
         "moe_add_rms_norm": ([P, Z, P, P, P, F, I, I, I, P, P, P, P], I),
         "moe_rope_cos_sin_table": ([P, I, I, ctypes.c_double, P], I),
@@ -98,7 +101,7 @@ EXPORTED = ("moe_route_topk_plus_shared", "moe_align_by_expert", "moe_fused_ffn"
             "srmoe_status_string", "srmoe_last_hip_error", "moe_workspace_bytes", "moe_status_string",
             "moe_layer_forward_staged", "moe_layer_forward_noalloc", "srmoe_source_hash", "moe_kv_append",
             "moe_tree_attention", "moe_prefill_attention", "moe_attention_workspace_bytes", "moe_window_attention",
-            "moe_add_rms_norm")
+            "moe_add_rms_norm", "moe_kv_usage", "moe_kv_usage_workspace_bytes", "moe_kv_evict")
 
 
 def _ptr(t):
@@ -369,3 +372,27 @@ def moe_window_attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scal
                                   _ptr(kv_lens), window, sinks, S, T, max_q, num_q_heads, num_kv_heads, head_dim, scale,
                                   softcap, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
     return _check("moe_window_attention", st) if check else st
+
+
+def moe_kv_usage_workspace_bytes(S, T, max_q, num_q_heads, num_kv_heads, head_dim):
+    return lib.moe_kv_usage_workspace_bytes(S, T, max_q, num_q_heads, num_kv_heads, head_dim)
+
+
+def moe_kv_usage(q, q_stride, k_cache, kv_type, k_scale, num_pages, page_size, page_stride, block_table, max_pages, cu_q,
+                 kv_lens, prefix_lens, lse, S, T, max_q, num_q_heads, num_kv_heads, head_dim, scale, softcap, prev, decay,
+                 usage, usage_rows, rows, workspace, ws_bytes, stream=None, check=True):
+    st = lib.moe_kv_usage(_ptr(q), q_stride, _ptr(k_cache), kv_type, _ptr(k_scale), num_pages, page_size, page_stride,
+                          _ptr(block_table), max_pages, _ptr(cu_q), _ptr(kv_lens), _ptr(prefix_lens), _ptr(lse), S, T,
+                          max_q, num_q_heads, num_kv_heads, head_dim, scale, softcap, _ptr(prev), decay, _ptr(usage),
+                          _ptr(usage_rows), rows, _ptr(workspace), ws_bytes, _stream(stream))
+    return _check("moe_kv_usage", st) if check else st
+
+
+def moe_kv_evict(k_cache, v_cache, kv_type, num_pages, page_size, page_stride, block_table, max_pages, kv_lens, usage,
+                 new_usage, usage_rows, rows, S, num_kv_heads, head_dim, limit, budget, sinks, recent, new_table,
+                 new_max_pages, new_lens, kept, stream=None, check=True):
+    st = lib.moe_kv_evict(_ptr(k_cache), _ptr(v_cache), kv_type, num_pages, page_size, page_stride, _ptr(block_table),
+                          max_pages, _ptr(kv_lens), _ptr(usage), _ptr(new_usage), _ptr(usage_rows), rows, S, num_kv_heads,
+                          head_dim, limit, budget, sinks, recent, _ptr(new_table), new_max_pages, _ptr(new_lens),
+                          _ptr(kept), _stream(stream))
+    return _check("moe_kv_evict", st) if check else st

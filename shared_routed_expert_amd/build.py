@@ -24,7 +24,8 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsrmoe.so")
 SOURCES = ["api.hip", "router.hip", "route.hip", "align.hip", "quant.hip", "ffn.hip", "ffn_decode.hip",
            "ffn_expert_decode.hip", "ffn_tile.hip", "front.hip", "qknorm.hip",
-           "kv_append.hip", "attention.hip", "attention_window.hip", "norm.hip"]
+           "kv_append.hip", "attention.hip", "attention_window.hip", "norm.hip",
+           "kv_usage.hip", "kv_evict.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -1,8 +1,8 @@
 """A paged key/value cache on the GPU and the calls that write and read it.
 
 Torch provides device memory and the stream (always torch's current stream of the cache's device); the
-writes (moe_kv_append) and the attention (moe_tree_attention, moe_prefill_attention, moe_window_attention) run in
-libsrmoe.so's HIP kernels. Every tensor starts on a 16-byte boundary, as torch allocates them; a slice that does not is
+writes (moe_kv_append) and the attention (moe_tree_attention, moe_prefill_attention, moe_window_attention), the
+tokens' usage and the eviction by it (moe_kv_usage, moe_kv_evict) run in libsrmoe.so's HIP kernels. Every tensor starts on a 16-byte boundary, as torch allocates them; a slice that does not is
 refused by name.
 """
 from __future__ import annotations
@@ -100,7 +100,8 @@ class PagedKVCache:
                   self.v_scale, self.num_pages, self.page_size, self.kv.stride(0))
         return q_out
 
-    def _attention(self, call, q, block_table, cu_q, kv_lens, extra, max_q, scale, softcap, out, lse):
+    def _queries(self, q, block_table, cu_q, kv_lens):
+        """Checks of what every call with queries takes; (S, T, q heads, max_pages)."""
         D = self.head_dim
         _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q is bf16 [T, q heads, head_dim]")
         T, Hq = q.shape[:2]
@@ -112,6 +113,11 @@ class PagedKVCache:
         self._tensor(block_table, "block_table", torch.int32, (S, max_pages))
         self._tensor(cu_q, "cu_q", torch.int32, (S + 1,))
         self._tensor(kv_lens, "kv_lens", torch.int32, (S,))
+        return S, T, Hq, max_pages
+
+    def _attention(self, call, q, block_table, cu_q, kv_lens, extra, max_q, scale, softcap, out, lse):
+        D = self.head_dim
+        S, T, Hq, max_pages = self._queries(q, block_table, cu_q, kv_lens)
         if out is None:
             out = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device=q.device)   # rows of no sequence are not written
         self._tensor(out, "out", torch.bfloat16, (T, Hq, D))
@@ -156,3 +162,62 @@ class PagedKVCache:
               "window is a whole number of at least 1, sinks of at least 0")
         return self._attention(L.moe_window_attention, q, block_table, cu_q, kv_lens, (window, sinks), max_q, scale,
                                softcap, out, lse)
+
+    def _usage_rows(self, usage, rows, S, max_pages, name="usage"):
+        _need(isinstance(usage, torch.Tensor) and usage.dim() == 3, f"{name} is float32 [rows, kv heads, tokens of a table's row]")
+        self._tensor(usage, name, torch.float32, (usage.shape[0], self.num_kv_heads, max_pages * self.page_size))
+        if rows is not None:
+            self._tensor(rows, "rows", torch.int32, (S,))
+        _need(usage.shape[0] >= (1 if rows is not None else S), f"{name} has a row for every sequence, or rows is given")
+
+    def usage(self, q, block_table, cu_q, kv_lens, max_q, lse, usage, prev=None, decay=1.0, rows=None, prefix_lens=None,
+              scale=None, softcap=0.0):
+        """The attention weight that each cached token gets from q (lse [T, q heads]: of the attention call on the same rows),
+        summed over the tokens and the heads of a kv head, plus decay * prev for the tokens before the call's own, into
+        usage [rows, kv heads, block_table.shape[1] * page_size] float32 (prev: None, usage itself or another array like
+        it; rows [S] int32: each sequence's row, None: its number). Sequences without tokens in q keep their row. Returns
+        usage."""
+        S, T, Hq, max_pages = self._queries(q, block_table, cu_q, kv_lens)
+        D = self.head_dim
+        self._tensor(lse, "lse", torch.float32, (T, Hq))
+        self._usage_rows(usage, rows, S, max_pages)
+        if prev is not None:
+            self._tensor(prev, "prev", torch.float32, usage.shape)
+        if prefix_lens is not None:
+            self._tensor(prefix_lens, "prefix_lens", torch.int32, (S,))
+        n = L.moe_kv_usage_workspace_bytes(S, T, max_q, Hq, self.num_kv_heads, D)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+        self._run(L.moe_kv_usage, q, q.stride(0) if T > 1 else Hq * D, self.k, self.kv_type, self.k_scale, self.num_pages,
+                  self.page_size, self.kv.stride(0), block_table, max_pages, cu_q, kv_lens, prefix_lens, lse, S, T, max_q, Hq,
+                  self.num_kv_heads, D, D ** -0.5 if scale is None else scale, softcap, prev, decay, usage, rows,
+                  usage.shape[0], ws, n)
+        return usage
+
+    def evict(self, block_table, kv_lens, usage, new_table, budget, limit=None, sinks=0, recent=0, rows=None,
+              new_usage=None):
+        """Cuts every sequence of more than `limit` tokens (budget unless given) to `budget`: each kv head keeps the first
+        `sinks`, the last `recent` and, between them, those of largest usage, in order, copied to the pages of new_table
+        [S, pages of the budget] int32, which no sequence may read in this call. usage is compacted into new_usage (itself
+        unless given). Returns (new_lens [S], kept [S, kv heads, budget]: old places of the kept tokens; -1 for a sequence
+        that is not cut). The caller takes new_table's row for the sequences that were cut and gives their old
+        pages back."""
+        _need(isinstance(block_table, torch.Tensor) and block_table.dim() == 2, "block_table is int32 [S, max_pages]")
+        S, max_pages = block_table.shape
+        self._tensor(block_table, "block_table", torch.int32, (S, max_pages))
+        self._tensor(kv_lens, "kv_lens", torch.int32, (S,))
+        _need(isinstance(new_table, torch.Tensor) and new_table.dim() == 2, "new_table is int32 [S, pages of the budget]")
+        self._tensor(new_table, "new_table", torch.int32, (S, new_table.shape[1]))
+        self._usage_rows(usage, rows, S, max_pages)
+        if new_usage is None:
+            new_usage = usage
+        self._tensor(new_usage, "new_usage", torch.float32, usage.shape)
+        limit = budget if limit is None else limit
+        _need(1 <= budget <= limit < 2 ** 31, "budget is at least 1 and at most limit")
+        _need(sinks >= 0 and recent >= 0 and sinks + recent <= budget, "sinks and recent fit into budget")
+        _need(new_table.shape[1] * self.page_size >= budget, "new_table's rows hold budget tokens")
+        new_lens = torch.empty_like(kv_lens)
+        kept = torch.full((S, self.num_kv_heads, budget), -1, dtype=torch.int32, device=kv_lens.device)
+        self._run(L.moe_kv_evict, self.k, self.v, self.kv_type, self.num_pages, self.page_size, self.kv.stride(0),
+                  block_table, max_pages, kv_lens, usage, new_usage, rows, usage.shape[0], S, self.num_kv_heads, self.head_dim,
+                  limit, budget, sinks, recent, new_table, new_table.shape[1], new_lens, kept)
+        return new_lens, kept

@@ -7,6 +7,7 @@
 
 #include "attention.hpp"
 #include "front_dev.hpp"
+#include "kv_usage.hpp"
 #include "norm.hpp"
 
 namespace srmoe {
@@ -832,12 +833,10 @@ size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, i
   return n > 256 ? n : 256;
 }
 
-static int attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
-                     const float* k_scale, const float* v_scale, int num_pages, int page_size, size_t page_stride,
-                     const int32_t* block_table, int max_pages, const int32_t* cu_q, const int32_t* kv_lens,
-                     const uint64_t* tree_mask, const int32_t* prefix_lens, int window, int sinks, int S, int T, int max_q,
-                     int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap, uint16_t* out,
-                     float* lse, void* workspace, size_t ws_bytes, void* stream) {   // window 0: none
+// Everything that the calls with queries over the cache refuse by its sizes; 0 if fine.
+static int check_attention_call(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim, int kv_type,
+                                int num_pages, int page_size, size_t page_stride, int max_pages, float scale,
+                                float softcap, size_t q_stride) {
   int st = check_attention_dims(S, T, max_q, num_q_heads, num_kv_heads, head_dim);
   if (st != SRMOE_OK) return st;
   st = check_cache_dims(kv_type, num_kv_heads, head_dim, num_pages, page_size, page_stride);
@@ -848,6 +847,18 @@ static int attention(const uint16_t* q, size_t q_stride, const void* k_cache, co
   if ((size_t)max_pages * page_size >= ((size_t)1 << 30)) return SRMOE_ERR_UNSUPPORTED;
   if (q_stride < (size_t)num_q_heads * head_dim || q_stride % 8 != 0 || q_stride >= ((size_t)1 << 40))
     return SRMOE_ERR_INVALID_ARG;
+  return SRMOE_OK;
+}
+
+static int attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,
+                     const float* k_scale, const float* v_scale, int num_pages, int page_size, size_t page_stride,
+                     const int32_t* block_table, int max_pages, const int32_t* cu_q, const int32_t* kv_lens,
+                     const uint64_t* tree_mask, const int32_t* prefix_lens, int window, int sinks, int S, int T, int max_q,
+                     int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap, uint16_t* out,
+                     float* lse, void* workspace, size_t ws_bytes, void* stream) {   // window 0: none
+  const int st = check_attention_call(S, T, max_q, num_q_heads, num_kv_heads, head_dim, kv_type, num_pages, page_size,
+                                      page_stride, max_pages, scale, softcap, q_stride);
+  if (st != SRMOE_OK) return st;
   if (T == 0 || S == 0) return SRMOE_OK;
   if (!q || !k_cache || !v_cache || !block_table || !cu_q || !kv_lens || !out || !workspace)
     return SRMOE_ERR_INVALID_ARG;
@@ -891,6 +902,73 @@ int moe_prefill_attention(const uint16_t* q, size_t q_stride, const void* k_cach
   return attention(q, q_stride, k_cache, v_cache, kv_type, k_scale, v_scale, num_pages, page_size, page_stride,
                    block_table, max_pages, cu_q, kv_lens, nullptr, prefix_lens, 0, 0, S, T, max_q, num_q_heads, num_kv_heads,
                    head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream);
+}
+
+size_t moe_kv_usage_workspace_bytes(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim) {
+  if (check_attention_dims(S, T, max_q, num_q_heads, num_kv_heads, head_dim) != SRMOE_OK) return 0;
+  return kv_usage_workspace_bytes(head_dim);
+}
+
+int moe_kv_usage(const uint16_t* q, size_t q_stride, const void* k_cache, int kv_type, const float* k_scale,
+                 int num_pages, int page_size, size_t page_stride, const int32_t* block_table, int max_pages,
+                 const int32_t* cu_q, const int32_t* kv_lens, const int32_t* prefix_lens, const float* lse, int S, int T,
+                 int max_q, int num_q_heads, int num_kv_heads, int head_dim, float scale, float softcap,
+                 const float* prev, float decay, float* usage, const int32_t* usage_rows, int rows, void* workspace,
+                 size_t ws_bytes, void* stream) {
+  const int st = check_attention_call(S, T, max_q, num_q_heads, num_kv_heads, head_dim, kv_type, num_pages, page_size,
+                                      page_stride, max_pages, scale, softcap, q_stride);
+  if (st != SRMOE_OK) return st;
+  if (!(decay >= 0.f) || !(decay <= 1.f) || rows < 1 || (!usage_rows && rows < S)) return SRMOE_ERR_INVALID_ARG;
+  if (T == 0 || S == 0) return SRMOE_OK;
+  if (!q || !k_cache || !block_table || !cu_q || !kv_lens || !lse || !usage || !workspace) return SRMOE_ERR_INVALID_ARG;
+  if (kv_type == SRMOE_KV_E4M3 && !k_scale) return SRMOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k_cache, k_scale, block_table, cu_q, kv_lens, prefix_lens, lse, prev, usage, usage_rows, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_kv_usage_workspace_bytes(S, T, max_q, num_q_heads, num_kv_heads, head_dim))
+    return SRMOE_ERR_WORKSPACE;
+  UsageArgs u{};
+  AttnArgs& a = u.a;
+  a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.k_scale = kv_type == SRMOE_KV_E4M3 ? k_scale : nullptr;
+  a.num_pages = num_pages; a.page_shift = __builtin_ctz((unsigned)page_size); a.page_stride = page_stride;
+  a.block_table = block_table; a.max_pages = max_pages; a.cu_q = cu_q; a.kv_lens = kv_lens; a.prefix_lens = prefix_lens;
+  a.S = S; a.T = T; a.max_q = max_q; a.Hq = num_q_heads; a.Hkv = num_kv_heads; a.G = num_q_heads / num_kv_heads;
+  a.D = head_dim; a.scale = scale; a.softcap = softcap; a.ws = workspace;
+  u.lse = lse; u.prev = prev; u.decay = decay; u.usage = usage; u.usage_rows = usage_rows; u.rows = rows;
+  return hip_status(launch_kv_usage(u, as_stream(stream)));
+}
+
+int moe_kv_evict(void* k_cache, void* v_cache, int kv_type, int num_pages, int page_size, size_t page_stride,
+                 const int32_t* block_table, int max_pages, const int32_t* kv_lens, const float* usage, float* new_usage,
+                 const int32_t* usage_rows, int rows, int S, int num_kv_heads, int head_dim, int limit, int budget,
+                 int sinks, int recent, const int32_t* new_table, int new_max_pages, int32_t* new_lens, int32_t* kept,
+                 void* stream) {
+  const int st = check_cache_dims(kv_type, num_kv_heads, head_dim, num_pages, page_size, page_stride);
+  if (st != SRMOE_OK) return st;
+  if (S < 0 || max_pages < 1 || new_max_pages < 1 || budget < 1 || limit < budget || sinks < 0 || recent < 0 ||
+      sinks > budget || recent > budget - sinks || rows < 1 || (!usage_rows && rows < S))
+    return SRMOE_ERR_INVALID_ARG;
+  // (one workgroup for each sequence and head, in one dimension of the grid)
+  if (S > 65536 || (long)S * num_kv_heads > 65535) return SRMOE_ERR_UNSUPPORTED;
+  if ((size_t)max_pages * page_size >= ((size_t)1 << 30) || (size_t)new_max_pages * page_size >= ((size_t)1 << 30))
+    return SRMOE_ERR_UNSUPPORTED;
+  if ((size_t)new_max_pages * page_size < (size_t)budget) return SRMOE_ERR_INVALID_ARG;
+  if (S == 0) return SRMOE_OK;
+  if (!k_cache || !v_cache || !block_table || !kv_lens || !usage || !new_usage || !new_table || !new_lens || !kept)
+    return SRMOE_ERR_INVALID_ARG;
+  if (new_lens == kv_lens || new_table == block_table) return SRMOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {k_cache, v_cache, block_table, kv_lens, usage, new_usage, usage_rows, new_table, new_lens, kept};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
+  const int es = kv_type == SRMOE_KV_E4M3 ? 1 : 2;
+  EvictArgs a{};
+  a.k_cache = static_cast<uint8_t*>(k_cache); a.v_cache = static_cast<uint8_t*>(v_cache); a.num_pages = num_pages;
+  a.page_shift = __builtin_ctz((unsigned)page_size); a.page_bytes = page_stride * es; a.row_bytes = head_dim * es;
+  a.block_table = block_table; a.max_pages = max_pages; a.kv_lens = kv_lens; a.usage = usage; a.new_usage = new_usage;
+  a.usage_rows = usage_rows; a.rows = rows; a.S = S; a.Hkv = num_kv_heads; a.limit = limit; a.budget = budget;
+  a.sinks = sinks; a.recent = recent; a.new_table = new_table; a.new_max_pages = new_max_pages; a.new_lens = new_lens;
+  a.kept = kept;
+  return hip_status(launch_kv_evict(a, as_stream(stream)));
 }
 
 int moe_window_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,

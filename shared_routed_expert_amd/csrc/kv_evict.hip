@@ -1,0 +1,258 @@
+// Eviction from the paged cache: per kv head, a sequence of n > limit cached tokens keeps its first `sinks`, its last
+// `recent`, and the m = budget - sinks - recent of largest usage between them (equal ones: the earlier), in order of position.
+//
+// Selection, one workgroup per sequence and kv head. Usage as an unsigned integer of the same order; the m-th largest is
+// found by three passes over the row (11, 11 and 10 bits, counted in LDS), which say what it is, T, and how many of the
+// values equal to T are kept, r. The place of token j among the kept is then (tokens before j that are protected or above T) +
+// min(r, tokens before j equal to T): counted per wave's stretch of the row, added up, and written out.
+//
+// The kept tokens' keys and values then go to the sequence's new pages, which no sequence reads in this call: every row is read
+// once and written once, by any workgroup at any time, and pages that other sequences share are left whole.
+#include "kv_usage.hpp"
+#include "common.hpp"
+
+namespace srmoe {
+
+constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
+constexpr int kBins = 2048, kCopies = 4;   // copies of the counts, a wave's own in four
+
+// Order of floats as that of unsigned integers: NaN lowest, then -infinity upwards, the zeros equal
+__device__ __forceinline__ uint32_t order_of(float v) {
+  if (v != v) return 0u;
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ int cached_tokens(const EvictArgs& a, int s) {
+  return min(max(a.kv_lens[s], 0), a.max_pages << a.page_shift);
+}
+
+__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs a) {
+  __shared__ uint32_t counts[kCopies][kBins];
+  __shared__ int wave_sum[kSelWaves], wave_eq[kSelWaves];
+  __shared__ int found_bin, found_left;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int s = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+  const int n = cached_tokens(a, s);
+  if (h == 0 && tid == 0) a.new_lens[s] = n > a.limit ? a.budget : n;
+  if (n <= a.limit) return;
+  const int row = a.usage_rows ? a.usage_rows[s] : s;
+  const bool known = row >= 0 && row < a.rows;   // without weights all are equal
+  const size_t base = ((size_t)(known ? row : 0) * a.Hkv + h) * ((size_t)a.max_pages << a.page_shift);
+  const float* const usage = a.usage + base;
+  const int lo = a.sinks, hi = n - a.recent;   // those that are chosen among
+  const int m = a.budget - a.sinks - a.recent;
+  // four tokens a lane (rows are 16-byte aligned, and as long as whole pages)
+  auto load4 = [&](int j, uint32_t (&o)[4]) {
+    const float4 v = known ? *reinterpret_cast<const float4*>(usage + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    o[0] = order_of(v.x); o[1] = order_of(v.y); o[2] = order_of(v.z); o[3] = order_of(v.w);
+  };
+
+  // -------- T, bits from the top, and r
+  uint32_t prefix = 0;
+  int left = m;   // how many of the values that begin with the prefix are kept
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
+    for (int i = tid; i < kCopies * kBins; i += kSelThreads) (&counts[0][0])[i] = 0;
+    __syncthreads();
+    uint32_t* const mine = counts[wave % kCopies];
+    for (int j0 = 0; j0 < hi; j0 += 4 * kSelThreads) {
+      const int j = j0 + 4 * tid;
+      uint32_t o[4] = {0, 0, 0, 0};
+      if (j < hi) load4(j, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = j + e >= lo && j + e < hi && (pass == 0 || o[e] >> (shift + (pass == 2 ? 10 : 11)) == prefix);
+        const uint32_t bin = (o[e] >> shift) & (bins - 1);
+        const uint64_t who = __ballot(in);
+        if (who == 0) continue;
+        // where all lanes count in one bin (values alike), one of them adds them all
+        const int lead = __ffsll((unsigned long long)who) - 1;
+        const uint32_t one = (uint32_t)__builtin_amdgcn_readlane((int)bin, lead);
+        if (__ballot(in && bin != one) == 0) {
+          if (lane == lead) atomicAdd(&mine[one], (uint32_t)__popcll(who));
+        } else if (in) {
+          atomicAdd(&mine[bin], 1u);
+        }
+      }
+    }
+    __syncthreads();
+    // the bin that holds the left-th largest: bins from the top, two a thread
+    const int b1 = bins - 1 - 2 * tid, b0 = b1 - 1;
+    int c1 = 0, c0 = 0;
+    if (b1 > 0) {
+#pragma unroll
+      for (int k = 0; k < kCopies; ++k) {
+        c1 += (int)counts[k][b1];
+        c0 += (int)counts[k][b0];
+      }
+    }
+    int incl = c1 + c0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 63) wave_sum[wave] = incl;
+    __syncthreads();
+    int above = incl - c1 - c0;
+    for (int k = 0; k < wave; ++k) above += wave_sum[k];
+    if (b1 > 0) {
+      if (left > above && left <= above + c1) {
+        found_bin = b1;
+        found_left = left - above;
+      } else if (left > above + c1 && left <= above + c1 + c0) {
+        found_bin = b0;
+        found_left = left - above - c1;
+      }
+    }
+    if (left == 0 && tid == 0) {   // none is chosen: the largest order there is, and none of it
+      found_bin = bins - 1;
+      found_left = 0;
+    }
+    __syncthreads();
+    prefix = pass == 2 ? prefix << 10 | (uint32_t)found_bin : prefix << 11 | (uint32_t)found_bin;
+    left = found_left;
+    __syncthreads();
+  }
+  const uint32_t T = prefix;
+
+  // -------- the places of the kept: a stretch of the row per wave
+  const int stretch = (n + 256 * kSelWaves - 1) / (256 * kSelWaves) * 256;
+  const int w_lo = min(wave * stretch, n), w_hi = min(w_lo + stretch, n);
+  auto look = [&](int j, uint32_t& above, uint32_t& equal) {   // bits of a lane's four tokens
+    above = equal = 0;
+    if (j >= w_hi) return;
+    uint32_t o[4];
+    load4(j, o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (j + e >= n) continue;
+      const bool safe = j + e < lo || j + e >= hi;
+      above |= (uint32_t)(safe || o[e] > T) << e;
+      equal |= (uint32_t)(!safe && o[e] == T) << e;
+    }
+  };
+  int n_above = 0, n_equal = 0;
+  for (int j0 = w_lo; j0 < w_hi; j0 += 256) {
+    uint32_t above, equal;
+    look(j0 + 4 * lane, above, equal);
+    n_above += __popc(above);
+    n_equal += __popc(equal);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    n_above += __shfl_xor(n_above, d, 64);
+    n_equal += __shfl_xor(n_equal, d, 64);
+  }
+  if (lane == 0) {
+    wave_sum[wave] = n_above;
+    wave_eq[wave] = n_equal;
+  }
+  __syncthreads();
+  n_above = n_equal = 0;
+  for (int k = 0; k < wave; ++k) {
+    n_above += wave_sum[k];
+    n_equal += wave_eq[k];
+  }
+  int32_t* const kept = a.kept + ((size_t)s * a.Hkv + h) * a.budget;
+  for (int j0 = w_lo; j0 < w_hi; j0 += 256) {
+    const int j = j0 + 4 * lane;
+    uint32_t above, equal;
+    look(j, above, equal);
+    // the lane's first token's places: sums over the lanes before
+    int pa = __popc(above), pe = __popc(equal);
+    const int own_a = pa, own_e = pe;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int oa = __shfl_up(pa, d, 64), oe = __shfl_up(pe, d, 64);
+      if (lane >= d) {
+        pa += oa;
+        pe += oe;
+      }
+    }
+    int at_a = n_above + pa - own_a, at_e = n_equal + pe - own_e;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool up = (above >> e) & 1, eq = (equal >> e) & 1;
+      if (up || (eq && at_e < left)) kept[at_a + min(at_e, left)] = j + e;
+      at_a += up;
+      at_e += eq;
+    }
+    n_above += __shfl(pa, 63, 64);
+    n_equal += __shfl(pe, 63, 64);
+  }
+
+  // -------- their usage, which may be written where it is read: place i is at most kept[i], so that a step's places lie
+  // before every later step's sources, and its own have all been read at the barrier
+  __threadfence_block();
+  __syncthreads();
+  if (!known) return;
+  float* const out = a.new_usage + base;
+  for (int i0 = 0; i0 < a.budget; i0 += 4 * kSelThreads) {
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kSelThreads + tid;
+      if (i < a.budget) v[k] = usage[kept[i]];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kSelThreads + tid;
+      if (i < a.budget) out[i] = v[k];
+    }
+  }
+}
+
+// Rows of keys and values to the new pages: 16 bytes a lane, kMoveRows rows of each per workgroup.
+constexpr int kMoveRows = 64;
+__global__ void __launch_bounds__(256) kv_move_kernel(const EvictArgs a, const int lanes /* of a row */, const int per_head) {
+  const int s = blockIdx.y / a.Hkv, h = blockIdx.y % a.Hkv;
+  const int n = cached_tokens(a, s);
+  if (n <= a.limit) return;
+  const int32_t* const kept = a.kept + ((size_t)s * a.Hkv + h) * a.budget;
+  const int at_once = 256 / lanes, mine = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int mask = (1 << a.page_shift) - 1;
+  const size_t rb = (size_t)lanes * 16, page_bytes = a.page_bytes;
+  for (int r = mine; r < kMoveRows; r += 4 * at_once) {
+    uint4 k[4], v[4];
+    size_t to[4];
+    bool go[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int row = r + x * at_once, i = blockIdx.x * kMoveRows + row;
+      go[x] = row < kMoveRows && i < a.budget;
+      k[x] = v[x] = make_uint4(0, 0, 0, 0);
+      if (!go[x]) continue;
+      const int j = kept[i];
+      const int src = a.block_table[(size_t)s * a.max_pages + (j >> a.page_shift)];
+      const int dst = a.new_table[(size_t)s * a.new_max_pages + (i >> a.page_shift)];
+      go[x] = dst >= 0 && dst < a.num_pages;
+      const size_t head = (size_t)h << a.page_shift;
+      to[x] = (size_t)(go[x] ? dst : 0) * page_bytes + (head + (i & mask)) * rb + lane * 16;
+      if (src >= 0 && src < a.num_pages) {   // (a token of no page becomes zeros)
+        const size_t from = (size_t)src * page_bytes + (head + (j & mask)) * rb + lane * 16;
+        k[x] = *reinterpret_cast<const uint4*>(a.k_cache + from);
+        v[x] = *reinterpret_cast<const uint4*>(a.v_cache + from);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (go[x]) {
+        *reinterpret_cast<uint4*>(a.k_cache + to[x]) = k[x];
+        *reinterpret_cast<uint4*>(a.v_cache + to[x]) = v[x];
+      }
+  }
+}
+
+hipError_t launch_kv_evict(const EvictArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(kv_select_kernel, dim3(a.S * a.Hkv), dim3(kSelThreads), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int blocks = (a.budget + kMoveRows - 1) / kMoveRows;
+  hipLaunchKernelGGL(kv_move_kernel, dim3(blocks, a.S * a.Hkv), dim3(256), 0, stream, a, a.row_bytes / 16, blocks);
+  return hipGetLastError();
+}
+
+}  // namespace srmoe
