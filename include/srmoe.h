@@ -488,7 +488,8 @@ size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, i
  * ones: the earlier; NaN counts as lowest; a sequence whose row is outside [0, rows): all are equal). The kept tokens stay
  * in order of position; the i-th one's key and value are copied to the i-th place of the sequence's new pages:
  *   new_table    [S, new_max_pages] int32, new_max_pages * page_size >= budget: pages that no sequence reads in this call and
- *                that stand nowhere else in it (they get other tokens than one expects otherwise). Of block_table
+ *                that stand nowhere else in it (they get other tokens than one expects otherwise); on any 4-byte boundary,
+ *                as a slice of a list of free pages may begin. Of block_table
  *                nothing changes: pages that sequences share stay whole, and the caller takes the sequence's new row and
  *                gives the old pages back. Tokens whose new page is outside the pool are not copied; tokens of a page outside
  *                it become zeros.

@@ -55,12 +55,13 @@ class PagedKVCache:
     def v(self):
         return self.kv[:, 1]
 
-    def _tensor(self, t, name, dtype, shape, strided=False):
+    def _tensor(self, t, name, dtype, shape, strided=False, slice_too=False):
         _need(isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape),
               f"{name} is {dtype} {list(shape)}")
         _need(strided or t.is_contiguous(), f"{name} is contiguous")
         _need(t.device == self.kv.device, f"{name} is on the cache's device")
-        _need_aligned(t, name)
+        if not slice_too:   # a contiguous slice may begin at any element
+            _need_aligned(t, name)
         return t
 
     def _run(self, call, *args):
@@ -206,7 +207,7 @@ class PagedKVCache:
         self._tensor(block_table, "block_table", torch.int32, (S, max_pages))
         self._tensor(kv_lens, "kv_lens", torch.int32, (S,))
         _need(isinstance(new_table, torch.Tensor) and new_table.dim() == 2, "new_table is int32 [S, pages of the budget]")
-        self._tensor(new_table, "new_table", torch.int32, (S, new_table.shape[1]))
+        self._tensor(new_table, "new_table", torch.int32, (S, new_table.shape[1]), slice_too=True)
         self._usage_rows(usage, rows, S, max_pages)
         if new_usage is None:
             new_usage = usage

@@ -957,7 +957,8 @@ int moe_kv_evict(void* k_cache, void* v_cache, int kv_type, int num_pages, int p
   if (!k_cache || !v_cache || !block_table || !kv_lens || !usage || !new_usage || !new_table || !new_lens || !kept)
     return SRMOE_ERR_INVALID_ARG;
   if (new_lens == kv_lens || new_table == block_table) return SRMOE_ERR_INVALID_ARG;
-  const void* ptrs[] = {k_cache, v_cache, block_table, kv_lens, usage, new_usage, usage_rows, new_table, new_lens, kept};
+  if (reinterpret_cast<uintptr_t>(new_table) & 3u) return SRMOE_ERR_INVALID_ARG;   // (a slice of a list of free pages)
+  const void* ptrs[] = {k_cache, v_cache, block_table, kv_lens, usage, new_usage, usage_rows, new_lens, kept};
   for (const void* p : ptrs)
     if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
   const int es = kv_type == SRMOE_KV_E4M3 ? 1 : 2;

@@ -224,6 +224,24 @@ def test_graph_replays_match_eager():
             assert torch.equal(got, want), rep
 
 
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_new_pages_from_a_slice(at):
+    """new_table may begin at any element of a list of free pages."""
+    c = Cut([300, 40], 64, 2, 128, 16, seed=12)
+    free = up(np.concatenate([np.full(at, -1, np.int32), c.new_table.flatten()]))
+    cache = PagedKVCache(c.kv.shape[0], 16, 2, 128, device=DEV)
+    cache.kv.copy_(up(c.kv).view(torch.bfloat16))
+    c.limit, c.sinks, c.recent = 64, 0, 1
+    c.d_kv, c.d_usage = cache.kv, up(c.usage)
+    c.d_new = torch.full_like(c.d_usage, GUARD)
+    lens, kept = cache.evict(up(c.table), up(np.array(c.kvs, np.int32)), c.d_usage, free[at:].view(2, 4), 64, recent=1,
+                             new_usage=c.d_new)
+    kept[1] = GUARD
+    c.d_kept = torch.cat([kept, torch.full((1, 2, 64), GUARD, dtype=torch.int32, device=DEV)])
+    c.d_lens = torch.cat([lens, torch.full((4,), GUARD, dtype=torch.int32, device=DEV)])
+    c.check(False)
+
+
 def test_cache_object():
     c = Cut([300, 40], 64, 2, 128, 16, seed=12)
     cache = PagedKVCache(c.kv.shape[0], 16, 2, 128, device=DEV)

@@ -66,7 +66,8 @@ def test_evict_rejects(L):
         assert evict(L, **kw) == -2, kw
     for name in ("k_cache", "v_cache", "block_table", "kv_lens", "usage", "new_usage", "new_table", "new_lens", "kept"):
         assert evict(L, **{name: None}) == -1, name
-        assert evict(L, **{name: MIS}) == -1, name
+        # (new_table: a slice of a list, at any of its elements)
+        assert evict(L, **{name: MIS if name != "new_table" else 0x10002}) == -1, name
     assert evict(L, usage_rows=MIS) == -1
     assert evict(L, S=0, k_cache=None) == 0
 
