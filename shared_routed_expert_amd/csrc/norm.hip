@@ -8,78 +8,97 @@
 
 namespace srmoe {
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
 // 8 bf16 values of a 16-byte word, widened
-__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void widen8(const i32x4& v, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    f[2 * i] = __uint_as_float((uint32_t)v[i] << 16);
+    f[2 * i + 1] = __uint_as_float((uint32_t)v[i] & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ i32x4 narrow8(const float (&f)[8]) {
+  return i32x4{(int)pack_bf16x2(f[0], f[1]), (int)pack_bf16x2(f[2], f[3]), (int)pack_bf16x2(f[4], f[5]),
+               (int)pack_bf16x2(f[6], f[7])};
 }
-
 enum Quant { kQuantNone, kQuantRow, kQuantBlock };
 
-// One workgroup of WAVES waves per row, thread t holding values 8 t .. 8 t + 7 of every stripe of 512 WAVES. STRIPES > 0:
-// the row's h stays in registers (H <= 512 WAVES STRIPES); 0: any H, x and r are read a second time.
-template <int WAVES, int STRIPES, Quant QUANT>
-__global__ void __launch_bounds__(64 * WAVES) add_rms_norm_kernel(const NormArgs a) {
-  __shared__ float red[2][WAVES];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const size_t t = blockIdx.x;
-  const uint16_t* const x = a.x + t * a.x_stride;
-  const uint16_t* const r = a.residual ? a.residual + t * a.H : nullptr;
-  constexpr int kKept = STRIPES > 0 ? STRIPES : 1;
-  constexpr int kStride = 512 * WAVES;
-  float h[kKept][8];
-  auto load = [&](int at, float (&f)[8]) {
-    widen8(*reinterpret_cast<const uint4*>(x + at), f);
-    if (r) {
-      float g[8];
-      widen8(*reinterpret_cast<const uint4*>(r + at), g);
+// LANES == 0: one workgroup per row; with W waves, thread t holds values 8 t .. 8 t + 7 of each of the row's STRIPES stripes of
+// 512 W. LANES > 0 (H <= 8 LANES): 256 / LANES rows per workgroup, with nothing to exchange between waves. All of a
+// row's loads are issued before the first is used, by addresses alone (lanes past the end load the row's first
+// values again and drop them): as branches they waited for each other, 16384 tokens of 5120 232 us instead of 132. x and the
+// residual are read once, and residual_out is next read a layer later, so they pass the caches by: 122 us, 6.2 TB/s. y and
+// xq are what the router and the experts read next (streamed as well: 129, and nothing gained behind them).
+template <int STRIPES, Quant QUANT, int LANES>
+__global__ void __launch_bounds__(STRIPES == 1 ? 256 : (STRIPES == 2 ? 512 : 1024)) add_rms_norm_kernel(const NormArgs a) {
+  constexpr int kWaves = STRIPES == 1 ? 4 : (STRIPES == 2 ? 8 : 16);   // at most
+  constexpr bool kKeepWeight = STRIPES < 8;                            // in registers
+  __shared__ float red[2][kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int tid = LANES ? threadIdx.x % LANES : threadIdx.x;           // among the row's threads
+  const int t = LANES ? blockIdx.x * (256 / LANES) + threadIdx.x / LANES : blockIdx.x;
+  const bool there = !LANES || t < a.T;
+  const size_t row = (size_t)(there ? t : a.T - 1) * a.H;
+  const uint16_t* const x = a.x + (size_t)(there ? t : a.T - 1) * a.x_stride;
+  int at[STRIPES];
+  bool in[STRIPES];
+  i32x4 xv[STRIPES], rv[STRIPES];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] += g[i];
-    }
+  for (int s = 0; s < STRIPES; ++s) {
+    at[s] = (s * (LANES ? LANES : blockDim.x) + tid) * 8;
+    in[s] = at[s] < a.H;
+    at[s] = in[s] ? at[s] : 0;
+    xv[s] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(x + at[s]));
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int s = 0; s < STRIPES; ++s)
+      rv[s] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(a.residual + row + at[s]));
+  }
+  auto weights = [&](int s, float (&w)[8]) {
+    const float4 p = *reinterpret_cast<const float4*>(a.weight + at[s]);
+    const float4 q = *reinterpret_cast<const float4*>(a.weight + at[s] + 4);
+    w[0] = p.x; w[1] = p.y; w[2] = p.z; w[3] = p.w; w[4] = q.x; w[5] = q.y; w[6] = q.z; w[7] = q.w;
   };
+  float w[STRIPES][8];
+  if (kKeepWeight) {
+#pragma unroll
+    for (int s = 0; s < STRIPES; ++s) weights(s, w[s]);
+  }
+  float h[STRIPES][8];
   float sum = 0.f, most = 0.f;
-  auto add = [&](int at, const float (&f)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i], f[i], sum);
-    if (QUANT == kQuantRow) {
+  for (int s = 0; s < STRIPES; ++s) {
+    widen8(xv[s], h[s]);
+    if (a.residual) {
+      float g[8];
+      widen8(rv[s], g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(f[i] * a.weight[at + i]));
+      for (int i = 0; i < 8; ++i) h[s][i] += g[i];
     }
-  };
-  if (STRIPES > 0) {
+    if (!kKeepWeight && QUANT == kQuantRow) weights(s, w[s]);
+    if (in[s]) {
 #pragma unroll
-    for (int s = 0; s < kKept; ++s) {
-      const int at = s * kStride + tid * 8;
-      if (at < a.H) {
-        load(at, h[s]);
-        add(at, h[s]);
+      for (int i = 0; i < 8; ++i) {
+        sum = __builtin_fmaf(h[s][i], h[s][i], sum);
+        if (QUANT == kQuantRow) most = fmaxf(most, fabsf(h[s][i] * w[s][i]));
       }
-    }
-  } else {
-    for (int at = tid * 8; at < a.H; at += kStride) {
-      load(at, h[0]);
-      add(at, h[0]);
     }
   }
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
-  if (QUANT == kQuantRow) most = wave_max(most);
-  if (WAVES > 1) {
+  for (int d = 1; d < (LANES ? LANES : 64); d <<= 1) {
+    sum += __shfl_xor(sum, d, 64);
+    if (QUANT == kQuantRow) most = fmaxf(most, __shfl_xor(most, d, 64));
+  }
+  if (!LANES) {
     if (lane == 0) {
       red[0][wave] = sum;
       red[1][wave] = most;
     }
     __syncthreads();
     sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i) {
+    for (int i = 0; i < waves; ++i) {
       sum += red[0][i];
       most = fmaxf(most, red[1][i]);
     }
@@ -88,49 +107,45 @@ __global__ void __launch_bounds__(64 * WAVES) add_rms_norm_kernel(const NormArgs
   float scale = 1.f;
   if (QUANT == kQuantRow) {
     scale = fp8_scale(most * rstd);
-    if (tid == 0) a.sx[t] = scale;
+    if (tid == 0 && there) a.sx[t] = scale;
   }
-  auto store = [&](int at, float (&f)[8], bool in) {
-    float y[8];
-    if (in && a.residual_out) *reinterpret_cast<uint4*>(a.residual_out + t * a.H + at) = narrow8(f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = in ? f[i] * rstd * a.weight[at + i] : 0.f;
-    if (in && a.y) *reinterpret_cast<uint4*>(a.y + t * a.H + at) = narrow8(y);
-    if (QUANT == kQuantNone) return;
-    if (QUANT == kQuantBlock) {   // 128 columns: 16 lanes
-      float m = 0.f;
+  for (int s = 0; s < STRIPES; ++s) {
+    if (!kKeepWeight) weights(s, w[s]);
+    float y[8], m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
-      scale = fp8_scale(row16_max(m));
-      if (in && (lane & 15) == 0) a.sx[t * (a.H / kGroup) + at / kGroup] = scale;
+    for (int i = 0; i < 8; ++i) {
+      y[i] = h[s][i] * rstd * w[s][i];
+      m = fmaxf(m, fabsf(y[i]));
     }
+    if (QUANT == kQuantBlock) scale = fp8_scale(row16_max(m));   // 128 columns: 16 lanes
+    if (!in[s] || !there) continue;
+    if (a.residual_out)
+      __builtin_nontemporal_store(narrow8(h[s]), reinterpret_cast<i32x4*>(a.residual_out + row + at[s]));
+    if (a.y) *reinterpret_cast<i32x4*>(a.y + row + at[s]) = narrow8(y);
+    if (QUANT == kQuantNone) continue;
+    if (QUANT == kQuantBlock && (lane & 15) == 0) a.sx[(row + at[s]) / kGroup] = scale;
     const ScaleDiv q = scale_div(scale);
-    if (in)
-      *reinterpret_cast<uint2*>(a.xq + t * a.H + at) = make_uint2(
-          quant2(q, y[0], y[1]) | quant2(q, y[2], y[3]) << 16, quant2(q, y[4], y[5]) | quant2(q, y[6], y[7]) << 16);
-  };
-  if (STRIPES > 0) {
-#pragma unroll
-    for (int s = 0; s < kKept; ++s) {
-      const int at = s * kStride + tid * 8;
-      store(at, h[s], at < a.H);
-    }
-  } else {
-    for (int base = 0; base < a.H; base += kStride) {
-      const int at = base + tid * 8;
-      if (at < a.H) load(at, h[0]);
-      store(at, h[0], at < a.H);
-    }
+    *reinterpret_cast<uint2*>(a.xq + row + at[s]) = make_uint2(
+        quant2(q, y[0], y[1]) | quant2(q, y[2], y[3]) << 16, quant2(q, y[4], y[5]) | quant2(q, y[6], y[7]) << 16);
   }
 }
 
 template <Quant QUANT>
 static hipError_t launch_quant(const NormArgs& a, hipStream_t stream) {
-  const dim3 grid(a.T);
-  if (a.H <= 2048) hipLaunchKernelGGL((add_rms_norm_kernel<4, 1, QUANT>), grid, dim3(256), 0, stream, a);
-  else if (a.H <= 4096) hipLaunchKernelGGL((add_rms_norm_kernel<4, 2, QUANT>), grid, dim3(256), 0, stream, a);
-  else if (a.H <= 8192) hipLaunchKernelGGL((add_rms_norm_kernel<4, 4, QUANT>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((add_rms_norm_kernel<8, 0, QUANT>), grid, dim3(512), 0, stream, a);
+  const int pieces = (a.H + 511) / 512;   // a wave's part of a stripe
+  auto whole = [&](auto* kernel, int stripes) {
+    hipLaunchKernelGGL(kernel, dim3(a.T), dim3(64 * ((pieces + stripes - 1) / stripes)), 0, stream, a);
+  };
+  auto several = [&](auto* kernel, int rows) {
+    hipLaunchKernelGGL(kernel, dim3((a.T + rows - 1) / rows), dim3(256), 0, stream, a);
+  };
+  if (a.H <= 128) several(add_rms_norm_kernel<1, QUANT, 16>, 16);
+  else if (a.H <= 512) several(add_rms_norm_kernel<1, QUANT, 64>, 4);
+  else if (pieces <= 4) whole(add_rms_norm_kernel<1, QUANT, 0>, 1);
+  else if (pieces <= 16) whole(add_rms_norm_kernel<2, QUANT, 0>, 2);
+  else if (pieces <= 64) whole(add_rms_norm_kernel<4, QUANT, 0>, 4);
+  else whole(add_rms_norm_kernel<8, QUANT, 0>, 8);
   return hipGetLastError();
 }
 
