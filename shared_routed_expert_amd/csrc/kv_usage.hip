@@ -16,6 +16,8 @@
 #include "kv_usage.hpp"
 #include "attention_common.hpp"
 
+#include <type_traits>
+
 namespace srmoe {
 
 // One sequence's key blocks: block b (of MB) is seen by the tokens from first(b) on.
@@ -51,7 +53,7 @@ struct alignas(32) UsageDesc {
 };
 
 constexpr int kUsageParts = 768;   // three workgroups on each CU
-constexpr int kUsageRows = 32;      // rows of a tile
+constexpr int kUsageRows = 64;     // rows of a tile
 
 // Where a sequence's weights are, or null: they are not kept
 __device__ __forceinline__ size_t usage_at(const UsageArgs& u, int s, int head, bool* kept) {
@@ -60,28 +62,102 @@ __device__ __forceinline__ size_t usage_at(const UsageArgs& u, int s, int head, 
   return ((size_t)(*kept ? row : 0) * u.a.Hkv + head) * ((size_t)u.a.max_pages << u.a.page_shift);
 }
 
+// lse log2 e = l2 + rest, the remainder as a factor; rows that saw nothing add nothing
+struct RowLse {
+  float l2, fix;
+};
+__device__ __forceinline__ RowLse row_lse_of(float lse) {
+  constexpr float kLog2eRest = 1.92596299112661746e-8f;   // log2 e minus its float32 value
+  if (lse == -INFINITY) lse = INFINITY;
+  const float l2 = lse * kLog2e;
+  const float rest = __builtin_fmaf(lse, kLog2e, -l2) + lse * kLog2eRest;
+  return {l2, __builtin_fabsf(l2) < 1e30f ? __builtin_amdgcn_exp2f(-rest) : 1.f};
+}
+
+// A key's 16 lanes added up: sums[t][e] of lane (quarter, col) is that of key 16 t + 4 quarter + e, row col; lane
+// (quarter, col) gets the sum of key 16 (col / 4) + 4 quarter + col % 4.
+template <int AT>
+__device__ __forceinline__ float column_sum(const float (&sums)[AT][4], int col) {
+  float v = 0.f;
+#pragma unroll
+  for (int t = 0; t < AT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x = sums[t][e];
+      x += dpp_f32<kDppXor1>(x);
+      x += dpp_f32<kDppXor2>(x);
+      x += dpp_f32<kDppRowHalfMirror>(x);
+      x += dpp_f32<kDppRowMirror>(x);
+      v = col == 4 * t + e ? x : v;
+    }
+  return v;
+}
+
+// 16 keys of a page, from the first one's row on, as the A operand of the score products
+template <int D, bool FP8>
+__device__ __forceinline__ void load_keys(const uint8_t* p, int lane, bf16x8 (&k)[D / 32]) {
+  p += (lane & 15) * (FP8 ? D : 2 * D) + (lane >> 4) * 16;
+  if constexpr (FP8) {   // 16 bytes are two steps' 8 values of this lane
+#pragma unroll
+    for (int st = 0; st < D / 32; st += 2) {
+      const i32x4 v = *reinterpret_cast<const i32x4*>(p + st * 32);
+      k[st] = bf16_of_e4m3(v[0], v[1]);
+      k[st + 1] = bf16_of_e4m3(v[2], v[3]);
+    }
+  } else {
+#pragma unroll
+    for (int st = 0; st < D / 32; ++st) k[st] = *reinterpret_cast<const bf16x8*>(p + st * 64);
+  }
+}
+// which 16-byte chunk of a row of q goes with step st of that
+template <bool FP8>
+__device__ __forceinline__ int q_chunk(int st, int quarter) {
+  return FP8 ? 8 * (st >> 1) + 2 * quarter + (st & 1) : 4 * st + quarter;
+}
+
+// r / G for r < 256, with magic = 2^16 / G + 1
+__device__ __forceinline__ int near_token(int r, uint32_t magic) { return (int)(__umul24((uint32_t)r, magic) >> 16); }
+
+template <Cap CAP>
+struct Weight {   // exp(z - lse) of a score q.k
+  float c, half_cap, cap2;
+  __device__ __forceinline__ Weight(const AttnArgs& a, float ks)
+      : c(CAP ? 2.f * kLog2e * a.scale * ks / a.softcap : a.scale * kLog2e * ks),
+        half_cap(0.5f * a.softcap),
+        cap2(a.softcap * kLog2e) {}
+  __device__ __forceinline__ float operator()(float dot, float l2) const {
+    return __builtin_amdgcn_exp2f(CAP ? capped<CAP == kCapLarge>(dot * c, half_cap, cap2) - l2
+                                      : __builtin_fmaf(dot, c, -l2));
+  }
+};
+
+// 16 bytes per lane from an address of its own to LDS address `lds` + 16 * lane (in asm: the compiler would wait for it
+// before any later LDS read)
+__device__ __forceinline__ void load_lds16_at(uint32_t lds, const void* p) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(uni((int)lds)), "v"(p) : "memory");
+}
+
 template <int D, bool FP8, Cap CAP>
 struct Usage {
   static constexpr int kWaves = 4, kThreads = 64 * kWaves;
   static constexpr int KPW = D == 256 ? 32 : 64;   // keys of a wave: 64 registers of them (32 for D = 64)
   static constexpr int KB = KPW * kWaves, AT = KPW / 16;
   static constexpr int STEPS = D / 32;
-  static constexpr int RB = D * (FP8 ? 1 : 2);
   static constexpr int CH = D / 8;                              // 16-byte chunks of a row of q
-  static constexpr int LOADS = kUsageRows * CH / kThreads;      // of a thread for a tile
+  static constexpr int RPL = 64 / CH;                           // rows of a wave's load (1 KB)
+  static constexpr int LOADS = kUsageRows / RPL / kWaves;       // of a wave for a tile
   // What a segment costs besides its rows, in rows (its keys, their sums)
   static constexpr int kSegCost = 64;
 };
 
 template <int D, bool FP8, Cap CAP>
-__global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3) kv_usage_kernel(const UsageArgs args, const uint64_t magic, const int parts_max,
-                                                          const bool joined, float* __restrict__ partials,
-                                                          UsageDesc* __restrict__ descs) {
+__global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3)
+kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic_near, const int parts_max,
+                float* __restrict__ partials, UsageDesc* __restrict__ descs) {
   using C = Usage<D, FP8, CAP>;
   const AttnArgs& a = args.a;
-  __shared__ __attribute__((aligned(16))) uint16_t qs[2][kUsageRows * D];
-  __shared__ float row_lse[2][kUsageRows], row_fix[2][kUsageRows];
-  __shared__ int row_lim[2][kUsageRows];
+  __shared__ __attribute__((aligned(1024))) uint16_t qs[2][kUsageRows * D];
+  __shared__ float row_l2[2][kUsageRows], row_fix[2][kUsageRows];
   __shared__ long scan_sum[C::kWaves];
   __shared__ long found_rem;
   __shared__ int found_s;
@@ -113,11 +189,10 @@ __global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3) kv_
   total = uni(total);
   const int parts = (int)min((long)parts_max, (total + C::kSegCost - 1) / C::kSegCost);
   const int w = xcd_tile((int)blockIdx.x, parts);   // consecutive parts on one XCD: neighbouring keys, the same rows
-  if (joined) {   // no segment begins in these parts until one is written below
-    if (blockIdx.x == 0)
-      for (int i = parts + tid; i < parts_max; i += C::kThreads) descs[i] = UsageDesc{0, 0, 0, 0, 0, 0};
-    if (w >= 0 && tid == 0) descs[w] = UsageDesc{0, 0, 0, 0, 0, 0};
-  }
+  // no segment begins in these parts until one is written below
+  if (blockIdx.x == 0)
+    for (int i = parts + tid; i < parts_max; i += C::kThreads) descs[i] = UsageDesc{0, 0, 0, 0, 0, 0};
+  if (w >= 0 && tid == 0) descs[w] = UsageDesc{0, 0, 0, 0, 0, 0};
   if (w < 0 || w >= parts) return;
   const Parts split(total, parts);
   long u = split.begin(w);
@@ -162,13 +237,16 @@ __global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3) kv_
 
   const int page_mask = (1 << a.page_shift) - 1;
   const size_t page_bytes = a.page_stride * (FP8 ? 1 : 2);
+  const uint32_t qs_off = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)&qs[0][0];
+  // chunk c of row r sits at c ^ swizzle(r): 16 rows' same chunk on different banks (D = 64: two rows span the 64 banks)
+  auto swizzle = [](int r) { return D == 64 ? (r >> 1) & 7 : r & 15; };
   int buf = 0;
   while (u < u_end) {
     // -------- the segment: its rows, and this part's share of their tiles (the fixed cost comes first; a part whose share
     // of the front is no tile leaves the segment to the next one, which then begins it)
     const int k0 = kb * C::KB;
     const int i0 = seq.first(kb, C::KB);
-    const int rows = (seq.n - i0) * a.G, r0 = i0 * a.G;
+    const int rows = (seq.n - i0) * a.G, r0 = i0 * a.G, r_end = seq.n * a.G;
     const long seg_end = u - rem + rows + C::kSegCost;
     const bool ends = seg_end <= u_end;
     const int ntiles = (rows + kUsageRows - 1) / kUsageRows;
@@ -176,9 +254,35 @@ __global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3) kv_
     const int t1 = ends ? ntiles : (int)(max(rem + u_end - u - C::kSegCost, 0l) / kUsageRows);
     const bool begins = ntiles > 0 ? t0 == 0 : rem == 0;
     if (ntiles > 0 ? t1 > 0 : begins) {
-      const float ks = FP8 ? a.k_scale[h] : 1.f;
-      const float c = CAP ? 2.f * kLog2e * a.scale * ks / a.softcap : a.scale * kLog2e * ks;
-      const float cap2 = a.softcap * kLog2e, half_cap = 0.5f * a.softcap;
+      const Weight<CAP> weight(a, FP8 ? a.k_scale[h] : 1.f);
+      // -------- rows of tile t to LDS, and their lse, which one wave takes at a time
+      const uint16_t* const qh = a.q + (size_t)seq.row0 * a.q_stride + (size_t)h * a.G * D;
+      auto token_of = [&](int r) { return (int)((uint64_t)r * magic >> 40); };   // r / G
+      float ahead = INFINITY;   // the lse of the next tile's row `lane`, in the wave whose turn it is
+      auto fetch = [&](int t, int b) {
+        const int first = r0 + t * kUsageRows, tok0 = uni(token_of(first)), last = min(kUsageRows, r_end - first) - 1;
+        const uint16_t* const q0 = qh + (size_t)tok0 * a.q_stride;
+        const int lead = first - tok0 * a.G;   // rows of its first token before the tile
+#pragma unroll
+        for (int y = 0; y < C::LOADS; ++y) {
+          const int x = y * C::kWaves + wave;   // (rows past the last repeat it)
+          const int at = x * C::RPL + lane / C::CH, r = lead + min(at, last), tok = near_token(r, magic_near);
+          const uint16_t* p = q0 + (size_t)(uint32_t)tok * a.q_stride + (r - tok * a.G) * D;
+          load_lds16_at(qs_off + b * (kUsageRows * D * 2) + x * 1024, p + ((lane % C::CH) ^ swizzle(at)) * 8);
+        }
+        if (wave == (t & 3)) {
+          const int r = lead + min(lane, last), tok = near_token(r, magic_near);
+          ahead = args.lse[(size_t)(seq.row0 + tok0 + tok) * a.Hq + h * a.G + r - tok * a.G];
+          if (lane > last) ahead = INFINITY;
+        }
+      };
+      auto put_lse = [&](int t, int b) {
+        if (wave != (t & 3)) return;
+        const RowLse f = row_lse_of(ahead);
+        row_l2[b][lane] = f.l2;
+        row_fix[b][lane] = f.fix;
+      };
+      if (t0 < t1) fetch(t0, buf);
       // -------- this wave's keys: 16 of them lie in one page; those past the end and of pages outside the pool are read
       // from page 0 (every key has sums of its own, and theirs are dropped)
       const int wk = k0 + wave * C::KPW;
@@ -186,125 +290,61 @@ __global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3) kv_
       int id = my_key < seq.kv ? a.block_table[(size_t)s * a.max_pages + (my_key >> a.page_shift)] : -1;
       const uint32_t pages_ok = (uint32_t)__ballot(id >= 0 && id < a.num_pages) & ((1u << C::AT) - 1);
       if (id < 0 || id >= a.num_pages) id = 0;
-      const uint8_t* const kc = static_cast<const uint8_t*>(a.k_cache) + ((size_t)h << a.page_shift) * C::RB;
+      const uint8_t* const kc = static_cast<const uint8_t*>(a.k_cache) + ((size_t)h << a.page_shift) * (FP8 ? D : 2 * D);
       bf16x8 k[C::AT][C::STEPS];
       if (t0 < t1) {
 #pragma unroll
-        for (int t = 0; t < C::AT; ++t) {
-          const size_t at = (size_t)__builtin_amdgcn_readlane(id, t) * page_bytes +
-                            (size_t)((wk + 16 * t) & page_mask) * C::RB;
-          const uint8_t* p = kc + at + col * C::RB + quarter * 16;
-          if constexpr (FP8) {   // 16 bytes are two steps' 8 values of this lane
-#pragma unroll
-            for (int st = 0; st < C::STEPS; st += 2) {
-              const i32x4 v = *reinterpret_cast<const i32x4*>(p + st * 32);
-              k[t][st] = bf16_of_e4m3(v[0], v[1]);
-              k[t][st + 1] = bf16_of_e4m3(v[2], v[3]);
-            }
-          } else {
-#pragma unroll
-            for (int st = 0; st < C::STEPS; ++st) k[t][st] = *reinterpret_cast<const bf16x8*>(p + st * 64);
-          }
-        }
+        for (int t = 0; t < C::AT; ++t)
+          load_keys<D, FP8>(kc + (size_t)__builtin_amdgcn_readlane(id, t) * page_bytes +
+                                (size_t)((wk + 16 * t) & page_mask) * (FP8 ? D : 2 * D), lane, k[t]);
       }
-      // -------- rows, a tile ahead: chunk c of row r sits at c ^ (r & 15) (D = 64, two rows to LDS's 64 banks: (r >> 1) & 7)
-      i32x4 ahead[C::LOADS];
-      float ahead_lse = 0.f;
-      int ahead_lim = 0;
-      auto swizzle = [](int r) { return D == 64 ? (r >> 1) & 7 : r & 15; };
-      auto token_of = [&](int r) { return (int)((uint64_t)r * magic >> 40); };
-      const int r_end = seq.n * a.G;
-      auto fetch = [&](int t) {
-#pragma unroll
-        for (int y = 0; y < C::LOADS; ++y) {
-          const int x = y * C::kThreads + tid, r = min(r0 + t * kUsageRows + x / C::CH, r_end - 1);
-          const int tok = token_of(r);
-          const uint16_t* p = a.q + (size_t)(seq.row0 + tok) * a.q_stride + (size_t)(h * a.G + r - tok * a.G) * D;
-          ahead[y] = *reinterpret_cast<const i32x4*>(p + (x % C::CH) * 8);
-        }
-        if (tid < kUsageRows) {
-          const int r = r0 + t * kUsageRows + tid, tok = token_of(min(r, r_end - 1));
-          // rows past the last, and such as saw nothing, add nothing
-          ahead_lse = r < r_end ? args.lse[(size_t)(seq.row0 + tok) * a.Hq + h * a.G + r - tok * a.G] : INFINITY;
-          if (ahead_lse == -INFINITY) ahead_lse = INFINITY;
-          ahead_lim = max(seq.all, seq.ctx + tok) + 1;
-        }
-      };
-      auto put = [&](int b) {
-#pragma unroll
-        for (int y = 0; y < C::LOADS; ++y) {
-          const int x = y * C::kThreads + tid, r = x / C::CH;
-          *reinterpret_cast<i32x4*>(&qs[b][r * D + ((x % C::CH) ^ swizzle(r)) * 8]) = ahead[y];
-        }
-        if (tid < kUsageRows) {
-          // lse log2 e = l2 + rest
-          constexpr float kLog2eRest = 1.92596299112661746e-8f;
-          const float l2 = ahead_lse * kLog2e;
-          const float rest = __builtin_fmaf(ahead_lse, kLog2e, -l2) + ahead_lse * kLog2eRest;
-          row_lse[b][tid] = l2;
-          row_fix[b][tid] = __builtin_fabsf(l2) < 1e30f ? __builtin_amdgcn_exp2f(-rest) : 1.f;
-          row_lim[b][tid] = ahead_lim;
-        }
-      };
+      if (t0 < t1) put_lse(t0, buf);
       float sum[C::AT][4];
 #pragma unroll
       for (int t = 0; t < C::AT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[t][e] = 0.f;
-      if (t0 < t1) {
-        fetch(t0);
-        put(buf);
-      }
       for (int t = t0; t < t1; ++t) {
-        __syncthreads();   // this tile is there, and the other buffer's rows have been read
-        if (t + 1 < t1) fetch(t + 1);
-        const int first = r0 + t * kUsageRows;
+        // this tile is there, and the other buffer's rows have been read
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (t + 1 < t1) fetch(t + 1, buf ^ 1);
+        const int first = r0 + t * kUsageRows, tok0 = uni(token_of(first));
         // every key of this wave is seen by every row of the tile
-        const bool all_seen = wk + C::KPW <= seq.ctx + uni(token_of(first)) + 1 || wk + C::KPW <= seq.all + 1;
+        const bool all_seen = wk + C::KPW <= max(seq.ctx + tok0, seq.all) + 1;
+        const int groups = (min(kUsageRows, r_end - first) + 15) >> 4;
+        auto tile = [&](auto masked) {
+          for (int g = 0; g < groups; ++g) {
+            const int r = 16 * g + col;
+            bf16x8 q[C::STEPS];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (first + 16 * half >= r_end) break;
-          const int r = 16 * half + col;
-          bf16x8 q[C::STEPS];
+            for (int st = 0; st < C::STEPS; ++st)
+              q[st] = *reinterpret_cast<const bf16x8*>(&qs[buf][r * D + (q_chunk<FP8>(st, quarter) ^ swizzle(r)) * 8]);
+            const float l2 = row_l2[buf][r], fix = row_fix[buf][r];
+            // (rows past the last add nothing: their lse is infinite)
+            const int lim = masked ? max(seq.all, seq.ctx + token_of(min(first + r, r_end - 1))) + 1 - wk - 4 * quarter : 0;
 #pragma unroll
-          for (int st = 0; st < C::STEPS; ++st) {
-            const int chunk = FP8 ? 8 * (st >> 1) + 2 * quarter + (st & 1) : 4 * st + quarter;
-            q[st] = *reinterpret_cast<const bf16x8*>(&qs[buf][r * D + (chunk ^ swizzle(r)) * 8]);
-          }
-          const float l2 = row_lse[buf][r], fix = row_fix[buf][r];
-          const int lim = row_lim[buf][r];
+            for (int t4 = 0; t4 < C::AT; ++t4) {
+              v4f z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int t4 = 0; t4 < C::AT; ++t4) {
-            v4f z = {0.f, 0.f, 0.f, 0.f};
+              for (int st = 0; st < C::STEPS; ++st)
+                z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[t4][st], q[st], z, 0, 0, 0);
 #pragma unroll
-            for (int st = 0; st < C::STEPS; ++st) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[t4][st], q[st], z, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float p = __builtin_amdgcn_exp2f(CAP ? capped<CAP == kCapLarge>(z[e] * c, half_cap, cap2) - l2
-                                                   : __builtin_fmaf(z[e], c, -l2));
-              if (!all_seen) p = wk + 16 * t4 + 4 * quarter + e < lim ? p : 0.f;
-              sum[t4][e] = __builtin_fmaf(p, fix, sum[t4][e]);
+              for (int e = 0; e < 4; ++e) {
+                float p = weight(z[e], l2);
+                if (masked) p = 16 * t4 + e < lim ? p : 0.f;
+                sum[t4][e] = __builtin_fmaf(p, fix, sum[t4][e]);
+              }
             }
           }
-        }
+        };
+        if (all_seen) tile(std::false_type{});
+        else tile(std::true_type{});
         buf ^= 1;
-        if (t + 1 < t1) put(buf);
+        if (t + 1 < t1) put_lse(t + 1, buf);
       }
-      // -------- a key's sum over its 16 lanes; lane (quarter, col) takes key 16 (col / 4) + 4 quarter + col % 4
-      float v = 0.f;
-#pragma unroll
-      for (int t = 0; t < C::AT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sum[t][e];
-          x += dpp_f32<kDppXor1>(x);
-          x += dpp_f32<kDppXor2>(x);
-          x += dpp_f32<kDppRowHalfMirror>(x);
-          x += dpp_f32<kDppRowMirror>(x);
-          v = col == 4 * t + e ? x : v;
-        }
+      const float total_weight = column_sum<C::AT>(sum, col);
       if (col < 4 * C::AT) {
-        if (!((pages_ok >> (col >> 2)) & 1)) v = 0.f;
+        const float v = (pages_ok >> (col >> 2)) & 1 ? total_weight : 0.f;
         const int at = wave * C::KPW + 16 * (col >> 2) + 4 * quarter + (col & 3), j = k0 + at;
         if (begins && (ends || ntiles == 0)) {
           bool kept;
@@ -315,7 +355,7 @@ __global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3) kv_
           partials[(size_t)(2 * w + (begins ? 1 : 0)) * C::KB + at] = v;
         }
       }
-      if (joined && tid == 0 && begins && !(ends || ntiles == 0))
+      if (tid == 0 && begins && !(ends || ntiles == 0))
         descs[w] = UsageDesc{s, h, k0, min(C::KB, seq.kv - k0), w, split.of(seg_end - 1)};
     }
 
@@ -329,6 +369,147 @@ __global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3) kv_
         do seq = uniform(seq_blocks(a, ++s, C::KB));
         while (seq.MB == 0);
       }
+    }
+  }
+}
+
+// Few rows per sequence and kv head (GROUPS times 16; a decoding step): every wave walks a stretch of 16-key tiles of its own,
+// the rows in its registers. The stretches are equal parts of all sequences' and heads' tiles laid end to end; a
+// tile is one wave's, so nothing is joined. Bound by the keys' bytes.
+constexpr int kFewWaves = 4096;   // four on every SIMD
+template <int D, bool FP8, Cap CAP, int GROUPS>
+__global__ void __launch_bounds__(256, D == 256 || GROUPS == 2 || CAP == kCapLarge ? 2 : 4)
+kv_usage_few_kernel(const UsageArgs args, const uint32_t magic_near) {
+  constexpr int KB = 16, AT = D == 256 ? 2 : 4, STEPS = D / 32;
+  const AttnArgs& a = args.a;
+  __shared__ long scan_sum[4];
+  __shared__ long found_rem[4];
+  __shared__ int found_s[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  const int col = lane & 15, quarter = lane >> 4;
+  const int per = (a.S + 255) / 256;
+  const int s_lo = min(tid * per, a.S), s_hi = min(s_lo + per, a.S);
+  long mine = 0;
+  for (int s = s_lo; s < s_hi; ++s) mine += (long)seq_blocks(a, s, KB).MB * a.Hkv;
+  long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const long o = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) scan_sum[wave] = incl;
+  __syncthreads();
+  long total = 0, before = incl - mine;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < wave) before += scan_sum[i];
+    total += scan_sum[i];
+  }
+  total = uni(total);
+  const int block = xcd_tile((int)blockIdx.x, (int)gridDim.x);
+  const Parts split(total, 4 * (int)gridDim.x);
+  // the sequences in which this workgroup's waves begin
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long u = split.begin(4 * block + i);
+    if (mine > 0 && u >= before && u < before + mine) {
+      long r = u - before;
+      for (int at = s_lo; at < s_hi; ++at) {
+        const long cost = (long)seq_blocks(a, at, KB).MB * a.Hkv;
+        if (r < cost) {
+          found_s[i] = at;
+          found_rem[i] = r;
+          break;
+        }
+        r -= cost;
+      }
+    }
+  }
+  __syncthreads();
+  long u = split.begin(4 * block + wave);
+  const long u_end = split.begin(4 * block + wave + 1);
+  if (u >= u_end) return;
+  auto uniform = [](SeqBlocks t) {
+    t.row0 = uni(t.row0); t.n = uni(t.n); t.kv = uni(t.kv); t.ctx = uni(t.ctx); t.all = uni(t.all); t.MB = uni(t.MB);
+    return t;
+  };
+  int s = uni(found_s[wave]);
+  SeqBlocks seq = uniform(seq_blocks(a, s, KB));
+  int h, kb;
+  {
+    const long rem = uni(found_rem[wave]);
+    h = uni((int)div_pos(rem, seq.MB));
+    kb = uni((int)(rem - (long)h * seq.MB));
+  }
+  const int page_mask = (1 << a.page_shift) - 1;
+  const size_t page_bytes = a.page_stride * (FP8 ? 1 : 2);
+  while (u < u_end) {
+    // -------- one sequence and head: its rows, then its tiles, AT at a time
+    const int rows = seq.n * a.G, tiles = (int)min((long)(seq.MB - kb), u_end - u);
+    bf16x8 q[GROUPS][STEPS];
+    RowLse row[GROUPS];
+    int lim[GROUPS];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const int r = min(16 * g + col, rows - 1), tok = near_token(r, magic_near);
+      const uint16_t* p = a.q + (size_t)(seq.row0 + tok) * a.q_stride + (size_t)(h * a.G + r - tok * a.G) * D;
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st)
+        q[g][st] = *reinterpret_cast<const bf16x8*>(p + q_chunk<FP8>(st, quarter) * 8);
+      float l = args.lse[(size_t)(seq.row0 + tok) * a.Hq + h * a.G + r - tok * a.G];
+      if (16 * g + col >= rows) l = INFINITY;   // adds nothing
+      row[g] = row_lse_of(l);
+      lim[g] = max(seq.all, seq.ctx + tok) + 1;
+    }
+    const Weight<CAP> weight(a, FP8 ? a.k_scale[h] : 1.f);
+    const uint8_t* const kc = static_cast<const uint8_t*>(a.k_cache) + ((size_t)h << a.page_shift) * (FP8 ? D : 2 * D);
+    bool kept;
+    const size_t base = usage_at(args, s, h, &kept);
+    const int* const table = a.block_table + (size_t)s * a.max_pages;
+    int id = 0;
+    for (int t = 0; t < tiles; t += AT) {
+      if (t % 64 == 0) {   // page ids of 64 tiles at a time, one per lane
+        const int key = (kb + t + lane) * 16;
+        id = t + lane < tiles ? table[key >> a.page_shift] : -1;
+      }
+      const int k0 = (kb + t) * 16, here = min(AT, tiles - t);
+      const uint32_t pages_ok = (uint32_t)(__ballot(id >= 0 && id < a.num_pages) >> (t % 64)) & ((1u << AT) - 1);
+      bf16x8 k[AT][STEPS];
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {   // (tiles past the stretch and of pages outside the pool: page 0's, dropped)
+        const int page = (pages_ok >> i) & 1 ? __builtin_amdgcn_readlane(id, (t + i) % 64) : 0;
+        load_keys<D, FP8>(kc + (size_t)page * page_bytes + (size_t)((k0 + 16 * i) & page_mask) * (FP8 ? D : 2 * D), lane, k[i]);
+      }
+      const int at = 16 * (col >> 2) + 4 * quarter + (col & 3), j = k0 + at;
+      const bool mine_too = kept && col < 4 * here && j < seq.kv;
+      const float old = mine_too && args.prev && j < seq.ctx ? args.prev[base + j] : 0.f;
+      float sum[AT][4];
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[i][e] = 0.f;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+          v4f z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int st = 0; st < STEPS; ++st) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[i][st], q[g][st], z, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = k0 + 16 * i + 4 * quarter + e < lim[g] ? weight(z[e], row[g].l2) : 0.f;
+            sum[i][e] = __builtin_fmaf(p, row[g].fix, sum[i][e]);
+          }
+        }
+      const float v = column_sum<AT>(sum, col);
+      if (mine_too) args.usage[base + j] = __builtin_fmaf(args.decay, old, (pages_ok >> (col >> 2)) & 1 ? v : 0.f);
+    }
+    u += tiles;
+    kb = 0;
+    if (++h >= a.Hkv && u < u_end) {
+      h = 0;
+      do seq = uniform(seq_blocks(a, ++s, KB));
+      while (seq.MB == 0);
     }
   }
 }
@@ -358,14 +539,25 @@ template <int D, bool FP8, Cap CAP>
 static hipError_t launch_usage(const UsageArgs& u, hipStream_t stream) {
   using C = Usage<D, FP8, CAP>;
   const AttnArgs& a = u.a;
+  // r / G: r magic >> 40 where r < 2^20 G, r magic_near >> 16 where r < 256
+  const uint64_t magic = (1ull << 40) / (uint64_t)a.G + 1;
+  const uint32_t magic_near = (1u << 16) / (uint32_t)a.G + 1;
+  const long rows = (long)a.max_q * a.G;
+  if (rows <= 32) {
+    const long tiles = (long)a.S * a.Hkv * ((((long)a.max_pages << a.page_shift) + 15) / 16);   // at most
+    const int grid = (int)min((long)kFewWaves / 4, (tiles + 3) / 4);
+    if (rows <= 16)
+      hipLaunchKernelGGL((kv_usage_few_kernel<D, FP8, CAP, 1>), dim3(grid), dim3(256), 0, stream, u, magic_near);
+    else
+      hipLaunchKernelGGL((kv_usage_few_kernel<D, FP8, CAP, 2>), dim3(grid), dim3(256), 0, stream, u, magic_near);
+    return hipGetLastError();
+  }
   float* partials = static_cast<float*>(a.ws);
   UsageDesc* descs = reinterpret_cast<UsageDesc*>(partials + 2 * (size_t)kUsageParts * C::KB);
-  const bool joined = (long)a.max_q * a.G > kUsageRows;   // (one tile is one part's)
-  const uint64_t magic = (1ull << 40) / (uint64_t)a.G + 1;   // row / G = row magic >> 40: row G < 2^40
-  hipLaunchKernelGGL((kv_usage_kernel<D, FP8, CAP>), dim3(kUsageParts), dim3(C::kThreads), 0, stream, u, magic, kUsageParts,
-                     joined, partials, descs);
+  hipLaunchKernelGGL((kv_usage_kernel<D, FP8, CAP>), dim3(kUsageParts), dim3(C::kThreads), 0, stream, u, magic, magic_near,
+                     kUsageParts, partials, descs);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !joined) return e;
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kv_usage_join_kernel, dim3(kUsageParts), dim3(C::KB), 0, stream, u, C::KB, (const float*)partials,
                      (const UsageDesc*)descs);
   return hipGetLastError();
