@@ -52,8 +52,7 @@ struct alignas(32) UsageDesc {
   int s, head, k0, keys, first, last;
 };
 
-constexpr int kUsageParts = 768;   // three workgroups on each CU
-constexpr int kUsageRows = 64;     // rows of a tile
+constexpr int kUsageParts = 512;   // two workgroups on each CU
 
 // Where a sequence's weights are, or null: they are not kept
 __device__ __forceinline__ size_t usage_at(const UsageArgs& u, int s, int head, bool* kept) {
@@ -76,11 +75,10 @@ __device__ __forceinline__ RowLse row_lse_of(float lse) {
 
 // A key's 16 lanes added up: sums[t][e] of lane (quarter, col) is that of key 16 t + 4 quarter + e, row col; lane
 // (quarter, col) gets the sum of key 16 (col / 4) + 4 quarter + col % 4.
-template <int AT>
-__device__ __forceinline__ float column_sum(const float (&sums)[AT][4], int col) {
+__device__ __forceinline__ float column_sum(const float (*sums)[4], int col) {
   float v = 0.f;
 #pragma unroll
-  for (int t = 0; t < AT; ++t)
+  for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float x = sums[t][e];
@@ -109,6 +107,42 @@ __device__ __forceinline__ void load_keys(const uint8_t* p, int lane, bf16x8 (&k
     for (int st = 0; st < D / 32; ++st) k[st] = *reinterpret_cast<const bf16x8*>(p + st * 64);
   }
 }
+// 32 of them, as the A operand of 32x32x16 products (pages hold 16 at least: two addresses)
+template <int D, bool FP8>
+__device__ __forceinline__ void load_keys32(const uint8_t* lo, const uint8_t* hi, int lane, bf16x8 (&k)[D / 16]) {
+  const uint8_t* p = (lane & 16 ? hi : lo) + (lane & 15) * (FP8 ? D : 2 * D) + (lane >> 5) * 16;
+  if constexpr (FP8) {   // 16 bytes are two steps' 8 values of this lane
+#pragma unroll
+    for (int st = 0; st < D / 16; st += 2) {
+      const i32x4 v = *reinterpret_cast<const i32x4*>(p + st * 16);
+      k[st] = bf16_of_e4m3(v[0], v[1]);
+      k[st + 1] = bf16_of_e4m3(v[2], v[3]);
+    }
+  } else {
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) k[st] = *reinterpret_cast<const bf16x8*>(p + st * 32);
+  }
+}
+template <bool FP8>
+__device__ __forceinline__ int q_chunk32(int st, int half) {
+  return FP8 ? 4 * (st >> 1) + 2 * half + (st & 1) : 2 * st + half;
+}
+// A key's 32 lanes added up, for two tiles: entry i of lane (half, row) is that of key 8 (i / 4) + 4 half + i % 4; the lane
+// with lane & 15 = i gets the sum of that key, of the odd tile where lane & 16.
+__device__ __forceinline__ float column_sum32(const float (&even)[16], const float (&odd)[16], int lane) {
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {   // the odd 16 lanes of the one against the even ones of the other
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(even[i]), __float_as_uint(odd[i]), false, false);
+    float x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    x += dpp_f32<kDppXor1>(x);
+    x += dpp_f32<kDppXor2>(x);
+    x += dpp_f32<kDppRowHalfMirror>(x);
+    x += dpp_f32<kDppRowMirror>(x);
+    v = (lane & 15) == i ? x : v;
+  }
+  return v;
+}
 // which 16-byte chunk of a row of q goes with step st of that
 template <bool FP8>
 __device__ __forceinline__ int q_chunk(int st, int quarter) {
@@ -131,39 +165,45 @@ struct Weight {   // exp(z - lse) of a score q.k
   }
 };
 
-// 16 bytes per lane from an address of its own to LDS address `lds` + 16 * lane (in asm: the compiler would wait for it
-// before any later LDS read)
+// 16 bytes per lane to LDS address `lds` + 16 * lane, from base + off, or from an address of its own (in asm: the compiler
+// would wait for it before any later LDS read)
 __device__ __forceinline__ void load_lds16_at(uint32_t lds, const void* p) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(uni((int)lds)), "v"(p) : "memory");
+}
+__device__ __forceinline__ void load_lds16_near(uint32_t lds, uint32_t off, const void* base) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(uni((int)lds)), "v"(off), "s"(uni((long)base))
+               : "memory");
 }
 
 template <int D, bool FP8, Cap CAP>
 struct Usage {
   static constexpr int kWaves = 4, kThreads = 64 * kWaves;
-  static constexpr int KPW = D == 256 ? 32 : 64;   // keys of a wave: 64 registers of them (32 for D = 64)
-  static constexpr int KB = KPW * kWaves, AT = KPW / 16;
-  static constexpr int STEPS = D / 32;
+  static constexpr int KPW = D == 256 ? 32 : 64;    // keys of a wave: 64 registers of them (32 for D = 64)
+  static constexpr int ROWS = D == 256 ? 64 : 128;  // rows of a tile
+  static constexpr int KB = KPW * kWaves, AT = KPW / 32;
+  static constexpr int STEPS = D / 16;
   static constexpr int CH = D / 8;                              // 16-byte chunks of a row of q
   static constexpr int RPL = 64 / CH;                           // rows of a wave's load (1 KB)
-  static constexpr int LOADS = kUsageRows / RPL / kWaves;       // of a wave for a tile
+  static constexpr int LOADS = ROWS / RPL / kWaves;       // of a wave for a tile
   // What a segment costs besides its rows, in rows (its keys, their sums)
-  static constexpr int kSegCost = 64;
+  static constexpr int kSegCost = 256;
+  static constexpr int LDS = 2 * ROWS * D * 2;
 };
 
 template <int D, bool FP8, Cap CAP>
-__global__ void __launch_bounds__(256, D == 256 || CAP == kCapLarge ? 2 : 3)
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic_near, const int parts_max,
                 float* __restrict__ partials, UsageDesc* __restrict__ descs) {
   using C = Usage<D, FP8, CAP>;
   const AttnArgs& a = args.a;
-  __shared__ __attribute__((aligned(1024))) uint16_t qs[2][kUsageRows * D];
-  __shared__ float row_l2[2][kUsageRows], row_fix[2][kUsageRows];
+  extern __shared__ __attribute__((aligned(1024))) uint16_t qs[];   // two tiles
+  __shared__ float row_l2[2][C::ROWS], row_fix[2][C::ROWS];
   __shared__ long scan_sum[C::kWaves];
   __shared__ long found_rem;
   __shared__ int found_s;
   __shared__ SeqBlocks found_seq;
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
-  const int col = lane & 15, quarter = lane >> 4;
+  const int col = lane & 31, half = lane >> 5;
   // -------- which part of the line of segments is this workgroup's: a stretch of sequences per thread
   const int per = (a.S + C::kThreads - 1) / C::kThreads;
   const int s_lo = min(tid * per, a.S), s_hi = min(s_lo + per, a.S);
@@ -237,9 +277,12 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
 
   const int page_mask = (1 << a.page_shift) - 1;
   const size_t page_bytes = a.page_stride * (FP8 ? 1 : 2);
-  const uint32_t qs_off = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)&qs[0][0];
+  const uint32_t qs_off = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)qs;
   // chunk c of row r sits at c ^ swizzle(r): 16 rows' same chunk on different banks (D = 64: two rows span the 64 banks)
   auto swizzle = [](int r) { return D == 64 ? (r >> 1) & 7 : r & 15; };
+  // bytes between a token's last row and the next token's first: 32-bit offsets within a tile where they are few
+  const bool near_rows = a.q_stride - (size_t)a.G * D < 1u << 22;
+  const uint32_t gap = (uint32_t)(a.q_stride - (size_t)a.G * D) * 2;
   int buf = 0;
   while (u < u_end) {
     // -------- the segment: its rows, and this part's share of their tiles (the fixed cost comes first; a part whose share
@@ -249,103 +292,156 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
     const int rows = (seq.n - i0) * a.G, r0 = i0 * a.G, r_end = seq.n * a.G;
     const long seg_end = u - rem + rows + C::kSegCost;
     const bool ends = seg_end <= u_end;
-    const int ntiles = (rows + kUsageRows - 1) / kUsageRows;
-    const int t0 = (int)(max(rem - C::kSegCost, 0l) / kUsageRows);
-    const int t1 = ends ? ntiles : (int)(max(rem + u_end - u - C::kSegCost, 0l) / kUsageRows);
+    const int ntiles = (rows + C::ROWS - 1) / C::ROWS;
+    const int t0 = (int)(max(rem - C::kSegCost, 0l) / C::ROWS);
+    const int t1 = ends ? ntiles : (int)(max(rem + u_end - u - C::kSegCost, 0l) / C::ROWS);
     const bool begins = ntiles > 0 ? t0 == 0 : rem == 0;
     if (ntiles > 0 ? t1 > 0 : begins) {
       const Weight<CAP> weight(a, FP8 ? a.k_scale[h] : 1.f);
       // -------- rows of tile t to LDS, and their lse, which one wave takes at a time
       const uint16_t* const qh = a.q + (size_t)seq.row0 * a.q_stride + (size_t)h * a.G * D;
       auto token_of = [&](int r) { return (int)((uint64_t)r * magic >> 40); };   // r / G
-      float ahead = INFINITY;   // the lse of the next tile's row `lane`, in the wave whose turn it is
+      float ahead = INFINITY;   // the lse of one of the next tile's rows, in the waves whose turn it is
       auto fetch = [&](int t, int b) {
-        const int first = r0 + t * kUsageRows, tok0 = uni(token_of(first)), last = min(kUsageRows, r_end - first) - 1;
+        const int first = r0 + t * C::ROWS, tok0 = uni(token_of(first)), last = min(C::ROWS, r_end - first) - 1;
         const uint16_t* const q0 = qh + (size_t)tok0 * a.q_stride;
         const int lead = first - tok0 * a.G;   // rows of its first token before the tile
 #pragma unroll
         for (int y = 0; y < C::LOADS; ++y) {
           const int x = y * C::kWaves + wave;   // (rows past the last repeat it)
           const int at = x * C::RPL + lane / C::CH, r = lead + min(at, last), tok = near_token(r, magic_near);
-          const uint16_t* p = q0 + (size_t)(uint32_t)tok * a.q_stride + (r - tok * a.G) * D;
-          load_lds16_at(qs_off + b * (kUsageRows * D * 2) + x * 1024, p + ((lane % C::CH) ^ swizzle(at)) * 8);
+          const uint32_t lds = qs_off + b * (C::ROWS * D * 2) + x * 1024, chunk = ((lane % C::CH) ^ swizzle(at)) * 16;
+          if (near_rows) load_lds16_near(lds, __umul24(tok, gap) + r * (2 * D) + chunk, q0);
+          else load_lds16_at(lds, reinterpret_cast<const uint8_t*>(q0 + tok * (a.q_stride - a.G * D) + r * D) + chunk);
         }
-        if (wave == (t & 3)) {
-          const int r = lead + min(lane, last), tok = near_token(r, magic_near);
+        if (tid / C::ROWS == t % (C::kThreads / C::ROWS)) {
+          const int r = lead + min(tid & (C::ROWS - 1), last), tok = near_token(r, magic_near);
           ahead = args.lse[(size_t)(seq.row0 + tok0 + tok) * a.Hq + h * a.G + r - tok * a.G];
-          if (lane > last) ahead = INFINITY;
         }
       };
-      auto put_lse = [&](int t, int b) {
-        if (wave != (t & 3)) return;
-        const RowLse f = row_lse_of(ahead);
-        row_l2[b][lane] = f.l2;
-        row_fix[b][lane] = f.fix;
+      auto put_lse = [&](int t, int b) {   // (not in fetch: a use of what it loads would wait for the rows as well)
+        if (tid / C::ROWS != t % (C::kThreads / C::ROWS)) return;
+        const int at = tid & (C::ROWS - 1);
+        const RowLse f = row_lse_of(r0 + t * C::ROWS + at < r_end ? ahead : INFINITY);
+        row_l2[b][at] = f.l2;
+        row_fix[b][at] = f.fix;
       };
       if (t0 < t1) fetch(t0, buf);
       // -------- this wave's keys: 16 of them lie in one page; those past the end and of pages outside the pool are read
       // from page 0 (every key has sums of its own, and theirs are dropped)
       const int wk = k0 + wave * C::KPW;
-      const int my_key = wk + 16 * (lane & (C::AT - 1));
+      const int my_key = wk + 16 * (lane & (2 * C::AT - 1));
       int id = my_key < seq.kv ? a.block_table[(size_t)s * a.max_pages + (my_key >> a.page_shift)] : -1;
-      const uint32_t pages_ok = (uint32_t)__ballot(id >= 0 && id < a.num_pages) & ((1u << C::AT) - 1);
+      const uint32_t pages_ok = (uint32_t)__ballot(id >= 0 && id < a.num_pages) & ((1u << 2 * C::AT) - 1);
       if (id < 0 || id >= a.num_pages) id = 0;
       const uint8_t* const kc = static_cast<const uint8_t*>(a.k_cache) + ((size_t)h << a.page_shift) * (FP8 ? D : 2 * D);
+      auto rows_of = [&](int i) {   // of the 16 keys from wk + 16 i on
+        return kc + (size_t)__builtin_amdgcn_readlane(id, i) * page_bytes +
+               (size_t)((wk + 16 * i) & page_mask) * (FP8 ? D : 2 * D);
+      };
       bf16x8 k[C::AT][C::STEPS];
       if (t0 < t1) {
 #pragma unroll
-        for (int t = 0; t < C::AT; ++t)
-          load_keys<D, FP8>(kc + (size_t)__builtin_amdgcn_readlane(id, t) * page_bytes +
-                                (size_t)((wk + 16 * t) & page_mask) * (FP8 ? D : 2 * D), lane, k[t]);
+        for (int t = 0; t < C::AT; ++t) load_keys32<D, FP8>(rows_of(2 * t), rows_of(2 * t + 1), lane, k[t]);
       }
       if (t0 < t1) put_lse(t0, buf);
-      float sum[C::AT][4];
+      // the keys are here before the loop: a wait for them inside would wait for the next tile's rows as well
 #pragma unroll
       for (int t = 0; t < C::AT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[t][e] = 0.f;
-      for (int t = t0; t < t1; ++t) {
+        for (int st = 0; st < C::STEPS; ++st) asm volatile("" ::"v"(__builtin_bit_cast(i32x4, k[t][st])));
+      float sum[C::AT][16];
+#pragma unroll
+      for (int t = 0; t < C::AT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[t][e] = 0.f;
+      auto step = [&](int t, auto masked) {
         // this tile is there, and the other buffer's rows have been read
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (t + 1 < t1) fetch(t + 1, buf ^ 1);
-        const int first = r0 + t * kUsageRows, tok0 = uni(token_of(first));
-        // every key of this wave is seen by every row of the tile
-        const bool all_seen = wk + C::KPW <= max(seq.ctx + tok0, seq.all) + 1;
-        const int groups = (min(kUsageRows, r_end - first) + 15) >> 4;
-        auto tile = [&](auto masked) {
-          for (int g = 0; g < groups; ++g) {
-            const int r = 16 * g + col;
-            bf16x8 q[C::STEPS];
+        const int first = r0 + t * C::ROWS, groups = (min(C::ROWS, r_end - first) + 31) >> 5;
+        const uint16_t* const rows_q = qs + buf * (C::ROWS * D);
+        bf16x8 q[C::STEPS];
+        float l2 = 0.f, fix = 0.f, next_l2, next_fix;
+        auto read = [&](int g, int st) {
+          const int r = 32 * g + col;
+          q[st] = *reinterpret_cast<const bf16x8*>(&rows_q[r * D + (q_chunk32<FP8>(st, half) ^ swizzle(r)) * 8]);
+        };
+        auto read_lse = [&](int g) {
+          next_l2 = row_l2[buf][32 * g + col];
+          next_fix = row_fix[buf][32 * g + col];
+        };
+        v16f z[2];
+        // A stage: the weights of 32 keys and 32 rows beside the products of the next 32 keys, or of the next rows' first
+        // ones; a group's last products hand their operands' registers to the next group's rows as they go.
+        auto group = [&](int g, auto last) {
+          // (rows past the last add nothing: their lse is infinite)
+          const int lim =
+              masked ? max(seq.all, seq.ctx + token_of(min(first + 32 * g + col, r_end - 1))) + 1 - wk - 4 * half : 0;
+          l2 = next_l2;
+          fix = next_fix;
 #pragma unroll
-            for (int st = 0; st < C::STEPS; ++st)
-              q[st] = *reinterpret_cast<const bf16x8*>(&qs[buf][r * D + (q_chunk<FP8>(st, quarter) ^ swizzle(r)) * 8]);
-            const float l2 = row_l2[buf][r], fix = row_fix[buf][r];
-            // (rows past the last add nothing: their lse is infinite)
-            const int lim = masked ? max(seq.all, seq.ctx + token_of(min(first + r, r_end - 1))) + 1 - wk - 4 * quarter : 0;
+          for (int i = 0; i < C::AT; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            const bool hand_over = !last && i + 2 == C::AT;
+            const bool products = C::AT > 1 && (i + 1 < C::AT || !last);   // (one tile: nothing to stand beside)
+            const int next = (i + 1) % C::AT;
+            if (products) {
+              z[next & 1] = v16f{};
 #pragma unroll
-            for (int t4 = 0; t4 < C::AT; ++t4) {
-              v4f z = {0.f, 0.f, 0.f, 0.f};
+              for (int st = 0; st < C::STEPS; ++st) {
+                z[next & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[next][st], q[st], z[next & 1], 0, 0, 0);
+                if (hand_over) read(g + 1, st);
+              }
+              if (hand_over) read_lse(g + 1);
+            }
 #pragma unroll
-              for (int st = 0; st < C::STEPS; ++st)
-                z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[t4][st], q[st], z, 0, 0, 0);
+            for (int e = 0; e < 16; ++e) {
+              float p = weight(z[i & 1][e], l2);
+              if (masked) p = 32 * i + 8 * (e / 4) + e % 4 < lim ? p : 0.f;
+              sum[i][e] = __builtin_fmaf(p, fix, sum[i][e]);
+            }
+            if (products && !masked && CAP == kCapNone) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float p = weight(z[e], l2);
-                if (masked) p = 16 * t4 + e < lim ? p : 0.f;
-                sum[t4][e] = __builtin_fmaf(p, fix, sum[t4][e]);
+              for (int x = 0; x < C::STEPS; ++x) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a product
+                if (hand_over) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 48 / C::STEPS, 0);
               }
             }
           }
         };
-        if (all_seen) tile(std::false_type{});
-        else tile(std::true_type{});
+        auto begin = [&](int g) {
+#pragma unroll
+          for (int st = 0; st < C::STEPS; ++st) read(g, st);
+          read_lse(g);
+          z[0] = v16f{};
+#pragma unroll
+          for (int st = 0; st < C::STEPS; ++st)
+            z[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[0][st], q[st], z[0], 0, 0, 0);
+        };
+        if constexpr (C::AT == 1) {
+          for (int g = 0; g < groups; ++g) {
+            begin(g);
+            group(g, std::true_type{});
+          }
+        } else {
+          begin(0);
+          for (int g = 0; g + 1 < groups; ++g) group(g, std::false_type{});
+          group(groups - 1, std::true_type{});
+        }
         buf ^= 1;
         if (t + 1 < t1) put_lse(t + 1, buf);
-      }
-      const float total_weight = column_sum<C::AT>(sum, col);
-      if (col < 4 * C::AT) {
-        const float v = (pages_ok >> (col >> 2)) & 1 ? total_weight : 0.f;
-        const int at = wave * C::KPW + 16 * (col >> 2) + 4 * quarter + (col & 3), j = k0 + at;
+      };
+      // later rows see more: once a tile's first row sees every key of this wave, all that follow do
+      int t = t0;
+      for (; t < t1 && wk + C::KPW > max(seq.ctx + uni(token_of(r0 + t * C::ROWS)), seq.all) + 1; ++t) step(t, std::true_type{});
+      for (; t < t1; ++t) step(t, std::false_type{});
+      const float total_weight = column_sum32(sum[0], sum[C::AT - 1], lane);   // (every lane takes part)
+      if (C::AT == 2 || col < 16) {
+        const int in_wave = 32 * (col >> 4) + 8 * ((col & 15) >> 2) + 4 * half + (col & 3);
+        const float v = (pages_ok >> (in_wave >> 4)) & 1 ? total_weight : 0.f;
+        const int at = wave * C::KPW + in_wave, j = k0 + at;
         if (begins && (ends || ntiles == 0)) {
           bool kept;
           const size_t base = usage_at(args, s, h, &kept);
@@ -380,7 +476,7 @@ constexpr int kFewWaves = 4096;   // four on every SIMD
 template <int D, bool FP8, Cap CAP, int GROUPS>
 __global__ void __launch_bounds__(256, D == 256 || GROUPS == 2 || CAP == kCapLarge ? 2 : 4)
 kv_usage_few_kernel(const UsageArgs args, const uint32_t magic_near) {
-  constexpr int KB = 16, AT = D == 256 ? 2 : 4, STEPS = D / 32;
+  constexpr int KB = 16, AT = 4, STEPS = D / 32;
   const AttnArgs& a = args.a;
   __shared__ long scan_sum[4];
   __shared__ long found_rem[4];
@@ -501,7 +597,7 @@ kv_usage_few_kernel(const UsageArgs args, const uint32_t magic_near) {
             sum[i][e] = __builtin_fmaf(p, row[g].fix, sum[i][e]);
           }
         }
-      const float v = column_sum<AT>(sum, col);
+      const float v = column_sum(sum, col);
       if (mine_too) args.usage[base + j] = __builtin_fmaf(args.decay, old, (pages_ok >> (col >> 2)) & 1 ? v : 0.f);
     }
     u += tiles;
@@ -515,7 +611,7 @@ kv_usage_few_kernel(const UsageArgs args, const uint32_t magic_near) {
 }
 
 // Adds the partial sums of segments that span several parts, in part order: workgroup w the one that begins in part w.
-__global__ void __launch_bounds__(256) kv_usage_join_kernel(const UsageArgs args, const int KB,
+__global__ void __launch_bounds__(512) kv_usage_join_kernel(const UsageArgs args, const int KB,
                                                             const float* __restrict__ partials,
                                                             const UsageDesc* __restrict__ descs) {
   const UsageDesc d = descs[blockIdx.x];
@@ -525,7 +621,13 @@ __global__ void __launch_bounds__(256) kv_usage_join_kernel(const UsageArgs args
   const size_t base = usage_at(args, d.s, d.head, &kept);
   if (!kept) return;
   float v = partials[(size_t)(2 * d.first + 1) * KB + at];
-  for (int p = d.first + 1; p <= d.last; ++p) v += partials[(size_t)(2 * p) * KB + at];
+  for (int p = d.first + 1; p <= d.last; p += 16) {   // 16 loads at a time
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = partials[(size_t)(2 * min(p + i, d.last)) * KB + at];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += p + i <= d.last ? x[i] : 0.f;
+  }
   const SeqInfo q = seq_info(args.a, d.s);
   args.usage[base + j] = args.prev && j < q.kv - q.tokens ? __builtin_fmaf(args.decay, args.prev[base + j], v) : v;
 }
@@ -554,7 +656,7 @@ static hipError_t launch_usage(const UsageArgs& u, hipStream_t stream) {
   }
   float* partials = static_cast<float*>(a.ws);
   UsageDesc* descs = reinterpret_cast<UsageDesc*>(partials + 2 * (size_t)kUsageParts * C::KB);
-  hipLaunchKernelGGL((kv_usage_kernel<D, FP8, CAP>), dim3(kUsageParts), dim3(C::kThreads), 0, stream, u, magic, magic_near,
+  hipLaunchKernelGGL((kv_usage_kernel<D, FP8, CAP>), dim3(kUsageParts), dim3(C::kThreads), C::LDS, stream, u, magic, magic_near,
                      kUsageParts, partials, descs);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
