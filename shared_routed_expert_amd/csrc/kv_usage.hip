@@ -91,23 +91,7 @@ __device__ __forceinline__ float column_sum(const float (*sums)[4], int col) {
   return v;
 }
 
-// 16 keys of a page, from the first one's row on, as the A operand of the score products
-template <int D, bool FP8>
-__device__ __forceinline__ void load_keys(const uint8_t* p, int lane, bf16x8 (&k)[D / 32]) {
-  p += (lane & 15) * (FP8 ? D : 2 * D) + (lane >> 4) * 16;
-  if constexpr (FP8) {   // 16 bytes are two steps' 8 values of this lane
-#pragma unroll
-    for (int st = 0; st < D / 32; st += 2) {
-      const i32x4 v = *reinterpret_cast<const i32x4*>(p + st * 32);
-      k[st] = bf16_of_e4m3(v[0], v[1]);
-      k[st + 1] = bf16_of_e4m3(v[2], v[3]);
-    }
-  } else {
-#pragma unroll
-    for (int st = 0; st < D / 32; ++st) k[st] = *reinterpret_cast<const bf16x8*>(p + st * 64);
-  }
-}
-// 32 of them, as the A operand of 32x32x16 products (pages hold 16 at least: two addresses)
+// 32 keys as the A operand of 32x32x16 products, from global memory (pages hold 16 at least: two addresses)
 template <int D, bool FP8>
 __device__ __forceinline__ void load_keys32(const uint8_t* lo, const uint8_t* hi, int lane, bf16x8 (&k)[D / 16]) {
   const uint8_t* p = (lane & 16 ? hi : lo) + (lane & 15) * (FP8 ? D : 2 * D) + (lane >> 5) * 16;
@@ -143,7 +127,7 @@ __device__ __forceinline__ float column_sum32(const float (&even)[16], const flo
   }
   return v;
 }
-// which 16-byte chunk of a row of q goes with step st of that
+// which 16-byte chunk of a row of q goes with step st of 16x16x32 products
 template <bool FP8>
 __device__ __forceinline__ int q_chunk(int st, int quarter) {
   return FP8 ? 8 * (st >> 1) + 2 * quarter + (st & 1) : 4 * st + quarter;
@@ -471,12 +455,24 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
 
 // Few rows per sequence and kv head (GROUPS times 16; a decoding step): every wave walks a stretch of 16-key tiles of its own,
 // the rows in its registers. The stretches are equal parts of all sequences' and heads' tiles laid end to end; a
-// tile is one wave's, so nothing is joined. Bound by the keys' bytes.
-constexpr int kFewWaves = 4096;   // four on every SIMD
+// tile is one wave's, so nothing is joined. Bound by the keys' bytes: they go to LDS in whole rows, 1 KB a load (straight to the
+// operand's registers, 64 bytes of a row at a time, 64 sequences of up to 8192 tokens took 22.1 us).
+template <int D, bool FP8>
+struct Few {
+  static constexpr int RB = D * (FP8 ? 1 : 2);                 // bytes of a key's row
+  static constexpr int CPR = RB / 16;                          // its 16-byte chunks
+  static constexpr int AT = RB == 512 ? 2 : 4;                 // tiles at a time
+  static constexpr int LOADS = AT * 16 * RB / 1024;
+  static constexpr int LDS = 4 * AT * 16 * RB;                 // of four waves
+  // chunk c of row r sits at c ^ swizzle(r): 16 rows' same chunk on different banks
+  static __device__ __forceinline__ int swizzle(int r) { return CPR >= 16 ? r & 15 : (CPR == 8 ? (r >> 1) & 7 : (r >> 2) & 3); }
+};
+constexpr int kFewWaves = 2048;   // two on every SIMD
 template <int D, bool FP8, Cap CAP, int GROUPS>
-__global__ void __launch_bounds__(256, D == 256 || GROUPS == 2 || CAP == kCapLarge ? 2 : 4)
-kv_usage_few_kernel(const UsageArgs args, const uint32_t magic_near) {
-  constexpr int KB = 16, AT = 4, STEPS = D / 32;
+__global__ void __launch_bounds__(256, 2) kv_usage_few_kernel(const UsageArgs args, const uint32_t magic_near) {
+  using F = Few<D, FP8>;
+  constexpr int KB = 16, AT = F::AT, STEPS = D / 32;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t stages[];
   const AttnArgs& a = args.a;
   __shared__ long scan_sum[4];
   __shared__ long found_rem[4];
@@ -539,6 +535,8 @@ kv_usage_few_kernel(const UsageArgs args, const uint32_t magic_near) {
   }
   const int page_mask = (1 << a.page_shift) - 1;
   const size_t page_bytes = a.page_stride * (FP8 ? 1 : 2);
+  uint8_t* const mine_lds = stages + wave * (F::LDS / 4);
+  const uint32_t mine_off = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)mine_lds;
   while (u < u_end) {
     // -------- one sequence and head: its rows, then its tiles, AT at a time
     const int rows = seq.n * a.G, tiles = (int)min((long)(seq.MB - kb), u_end - u);
@@ -570,33 +568,52 @@ kv_usage_few_kernel(const UsageArgs args, const uint32_t magic_near) {
       }
       const int k0 = (kb + t) * 16, here = min(AT, tiles - t);
       const uint32_t pages_ok = (uint32_t)(__ballot(id >= 0 && id < a.num_pages) >> (t % 64)) & ((1u << AT) - 1);
-      bf16x8 k[AT][STEPS];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the last tiles have been read
 #pragma unroll
-      for (int i = 0; i < AT; ++i) {   // (tiles past the stretch and of pages outside the pool: page 0's, dropped)
+      for (int x = 0; x < F::LOADS; ++x) {   // (tiles past the stretch and of pages outside the pool: page 0's, dropped)
+        constexpr int kRows = 1024 / F::RB;
+        const int i = x * kRows / 16, r = x * kRows % 16 + lane / F::CPR;
         const int page = (pages_ok >> i) & 1 ? __builtin_amdgcn_readlane(id, (t + i) % 64) : 0;
-        load_keys<D, FP8>(kc + (size_t)page * page_bytes + (size_t)((k0 + 16 * i) & page_mask) * (FP8 ? D : 2 * D), lane, k[i]);
+        const uint8_t* p = kc + (size_t)page * page_bytes + (size_t)((k0 + 16 * i) & page_mask) * F::RB;
+        load_lds16_near(mine_off + x * 1024, r * F::RB + (((lane % F::CPR) ^ F::swizzle(r)) << 4), p);
       }
       const int at = 16 * (col >> 2) + 4 * quarter + (col & 3), j = k0 + at;
       const bool mine_too = kept && col < 4 * here && j < seq.kv;
       const float old = mine_too && args.prev && j < seq.ctx ? args.prev[base + j] : 0.f;
-      float sum[AT][4];
+      float sum[4][4];
 #pragma unroll
-      for (int i = 0; i < AT; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[i][e] = 0.f;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g)
+      for (int i = 0; i < AT; ++i) {
+        bf16x8 k[STEPS];
+        const uint8_t* const rows_k = mine_lds + (16 * i + col) * F::RB;
+        auto chunk = [&](int c) { return *reinterpret_cast<const i32x4*>(rows_k + ((c ^ F::swizzle(col)) << 4)); };
+        if constexpr (FP8) {   // 16 bytes are two steps' 8 values of this lane
 #pragma unroll
-        for (int i = 0; i < AT; ++i) {
+          for (int st = 0; st < STEPS; st += 2) {
+            const i32x4 v = chunk(2 * st + quarter);
+            k[st] = bf16_of_e4m3(v[0], v[1]);
+            k[st + 1] = bf16_of_e4m3(v[2], v[3]);
+          }
+        } else {
+#pragma unroll
+          for (int st = 0; st < STEPS; ++st) k[st] = __builtin_bit_cast(bf16x8, chunk(4 * st + quarter));
+        }
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
           v4f z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int st = 0; st < STEPS; ++st) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[i][st], q[g][st], z, 0, 0, 0);
+          for (int st = 0; st < STEPS; ++st) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[st], q[g][st], z, 0, 0, 0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float p = k0 + 16 * i + 4 * quarter + e < lim[g] ? weight(z[e], row[g].l2) : 0.f;
             sum[i][e] = __builtin_fmaf(p, row[g].fix, sum[i][e]);
           }
         }
+      }
       const float v = column_sum(sum, col);
       if (mine_too) args.usage[base + j] = __builtin_fmaf(args.decay, old, (pages_ok >> (col >> 2)) & 1 ? v : 0.f);
     }
@@ -640,6 +657,7 @@ size_t kv_usage_workspace_bytes(int D) {
 template <int D, bool FP8, Cap CAP>
 static hipError_t launch_usage(const UsageArgs& u, hipStream_t stream) {
   using C = Usage<D, FP8, CAP>;
+  using F = Few<D, FP8>;
   const AttnArgs& a = u.a;
   // r / G: r magic >> 40 where r < 2^20 G, r magic_near >> 16 where r < 256
   const uint64_t magic = (1ull << 40) / (uint64_t)a.G + 1;
@@ -649,9 +667,9 @@ static hipError_t launch_usage(const UsageArgs& u, hipStream_t stream) {
     const long tiles = (long)a.S * a.Hkv * ((((long)a.max_pages << a.page_shift) + 15) / 16);   // at most
     const int grid = (int)min((long)kFewWaves / 4, (tiles + 3) / 4);
     if (rows <= 16)
-      hipLaunchKernelGGL((kv_usage_few_kernel<D, FP8, CAP, 1>), dim3(grid), dim3(256), 0, stream, u, magic_near);
+      hipLaunchKernelGGL((kv_usage_few_kernel<D, FP8, CAP, 1>), dim3(grid), dim3(256), F::LDS, stream, u, magic_near);
     else
-      hipLaunchKernelGGL((kv_usage_few_kernel<D, FP8, CAP, 2>), dim3(grid), dim3(256), 0, stream, u, magic_near);
+      hipLaunchKernelGGL((kv_usage_few_kernel<D, FP8, CAP, 2>), dim3(grid), dim3(256), F::LDS, stream, u, magic_near);
     return hipGetLastError();
   }
   float* partials = static_cast<float*>(a.ws);
