@@ -27,42 +27,61 @@ __device__ __forceinline__ int cached_tokens(const EvictArgs& a, int s) {
   return min(max(a.kv_lens[s], 0), a.max_pages << a.page_shift);
 }
 
-__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs a) {
-  __shared__ uint32_t counts[kCopies][kBins];
-  __shared__ int wave_sum[kSelWaves], wave_eq[kSelWaves];
-  __shared__ int found_bin, found_left;
+// What the workgroup shares.
+struct Select {
+  uint32_t counts[kCopies][kBins];
+  int wave_sum[kSelWaves], wave_eq[kSelWaves];
+  int found_bin, found_left;
+};
+
+// A wave takes a stretch of the row, 256 tokens at a time, four a lane. HELD > 0: the stretch is at most HELD such steps and
+// stays in registers (one read of the row: 2112 tokens 10.8 us with a read for each pass, see launch_kv_evict).
+template <int HELD>
+__device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const float* usage, float* out, int32_t* kept, int n) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int s = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
-  const int n = cached_tokens(a, s);
-  if (h == 0 && tid == 0) a.new_lens[s] = n > a.limit ? a.budget : n;
-  if (n <= a.limit) return;
-  const int row = a.usage_rows ? a.usage_rows[s] : s;
-  const bool known = row >= 0 && row < a.rows;   // without weights all are equal
-  const size_t base = ((size_t)(known ? row : 0) * a.Hkv + h) * ((size_t)a.max_pages << a.page_shift);
-  const float* const usage = a.usage + base;
   const int lo = a.sinks, hi = n - a.recent;   // those that are chosen among
-  const int m = a.budget - a.sinks - a.recent;
-  // four tokens a lane (rows are 16-byte aligned, and as long as whole pages)
-  auto load4 = [&](int j, uint32_t (&o)[4]) {
-    const float4 v = known ? *reinterpret_cast<const float4*>(usage + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-    o[0] = order_of(v.x); o[1] = order_of(v.y); o[2] = order_of(v.z); o[3] = order_of(v.w);
+  const int stretch = (n + 256 * kSelWaves - 1) / (256 * kSelWaves) * 256;
+  const int w_lo = min(wave * stretch, n), w_hi = min(w_lo + stretch, n);
+  const int steps = (w_hi - w_lo + 255) / 256;
+  // orders of the four tokens from j on (rows are 16-byte aligned, and as long as whole pages; no row: all are equal)
+  auto load4 = [&](int j) {
+    const float4 v = usage && j < w_hi ? *reinterpret_cast<const float4*>(usage + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_uint4(order_of(v.x), order_of(v.y), order_of(v.z), order_of(v.w));
+  };
+  constexpr int kKept = HELD > 0 ? HELD : 1;
+  uint4 held[kKept];
+  if (HELD > 0) {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) held[i] = load4(w_lo + 256 * i + 4 * lane);
+  }
+  auto each = [&](auto f) {   // f(first token of the lane's four, their orders)
+    if (HELD > 0) {
+#pragma unroll
+      for (int i = 0; i < kKept; ++i)
+        if (i < steps) f(w_lo + 256 * i + 4 * lane, held[i]);
+    } else {
+      for (int i = 0; i < steps; ++i) {
+        const int j = w_lo + 256 * i + 4 * lane;
+        f(j, load4(j));
+      }
+    }
   };
 
   // -------- T, bits from the top, and r
   uint32_t prefix = 0;
-  int left = m;   // how many of the values that begin with the prefix are kept
+  int left = a.budget - a.sinks - a.recent;   // how many of the values that begin with the prefix are kept
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
-    for (int i = tid; i < kCopies * kBins; i += kSelThreads) (&counts[0][0])[i] = 0;
+    uint4* const zero = reinterpret_cast<uint4*>(&sh.counts[0][0]);
+    for (int i = tid; i < kCopies * kBins / 4; i += kSelThreads) zero[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    uint32_t* const mine = counts[wave % kCopies];
-    for (int j0 = 0; j0 < hi; j0 += 4 * kSelThreads) {
-      const int j = j0 + 4 * tid;
-      uint32_t o[4] = {0, 0, 0, 0};
-      if (j < hi) load4(j, o);
+    uint32_t* const mine = sh.counts[wave % kCopies];
+    each([&](int j, const uint4& four) {
+      const uint32_t o[4] = {four.x, four.y, four.z, four.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool in = j + e >= lo && j + e < hi && (pass == 0 || o[e] >> (shift + (pass == 2 ? 10 : 11)) == prefix);
+        const bool in = j + e >= lo && j + e < min(hi, w_hi) &&
+                        (pass == 0 || o[e] >> (shift + (pass == 2 ? 10 : 11)) == prefix);
         const uint32_t bin = (o[e] >> shift) & (bins - 1);
         const uint64_t who = __ballot(in);
         if (who == 0) continue;
@@ -75,7 +94,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
           atomicAdd(&mine[bin], 1u);
         }
       }
-    }
+    });
     __syncthreads();
     // the bin that holds the left-th largest: bins from the top, two a thread
     const int b1 = bins - 1 - 2 * tid, b0 = b1 - 1;
@@ -83,8 +102,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
     if (b1 > 0) {
 #pragma unroll
       for (int k = 0; k < kCopies; ++k) {
-        c1 += (int)counts[k][b1];
-        c0 += (int)counts[k][b0];
+        c1 += (int)sh.counts[k][b1];
+        c0 += (int)sh.counts[k][b0];
       }
     }
     int incl = c1 + c0;
@@ -93,85 +112,78 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
       const int o = __shfl_up(incl, d, 64);
       if (lane >= d) incl += o;
     }
-    if (lane == 63) wave_sum[wave] = incl;
+    if (lane == 63) sh.wave_sum[wave] = incl;
     __syncthreads();
     int above = incl - c1 - c0;
-    for (int k = 0; k < wave; ++k) above += wave_sum[k];
+#pragma unroll
+    for (int k = 0; k < kSelWaves; ++k) above += k < wave ? sh.wave_sum[k] : 0;
     if (b1 > 0) {
       if (left > above && left <= above + c1) {
-        found_bin = b1;
-        found_left = left - above;
+        sh.found_bin = b1;
+        sh.found_left = left - above;
       } else if (left > above + c1 && left <= above + c1 + c0) {
-        found_bin = b0;
-        found_left = left - above - c1;
+        sh.found_bin = b0;
+        sh.found_left = left - above - c1;
       }
     }
     if (left == 0 && tid == 0) {   // none is chosen: the largest order there is, and none of it
-      found_bin = bins - 1;
-      found_left = 0;
+      sh.found_bin = bins - 1;
+      sh.found_left = 0;
     }
     __syncthreads();
-    prefix = pass == 2 ? prefix << 10 | (uint32_t)found_bin : prefix << 11 | (uint32_t)found_bin;
-    left = found_left;
-    __syncthreads();
+    prefix = prefix << (pass == 2 ? 10 : 11) | (uint32_t)sh.found_bin;
+    left = sh.found_left;
   }
   const uint32_t T = prefix;
 
-  // -------- the places of the kept: a stretch of the row per wave
-  const int stretch = (n + 256 * kSelWaves - 1) / (256 * kSelWaves) * 256;
-  const int w_lo = min(wave * stretch, n), w_hi = min(w_lo + stretch, n);
-  auto look = [&](int j, uint32_t& above, uint32_t& equal) {   // bits of a lane's four tokens
+  // -------- the places of the kept
+  auto look = [&](int j, const uint4& four, uint32_t& above, uint32_t& equal) {   // bits of a lane's four tokens
+    const uint32_t o[4] = {four.x, four.y, four.z, four.w};
     above = equal = 0;
-    if (j >= w_hi) return;
-    uint32_t o[4];
-    load4(j, o);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (j + e >= n) continue;
+      if (j + e >= w_hi) continue;
       const bool safe = j + e < lo || j + e >= hi;
       above |= (uint32_t)(safe || o[e] > T) << e;
       equal |= (uint32_t)(!safe && o[e] == T) << e;
     }
   };
   int n_above = 0, n_equal = 0;
-  for (int j0 = w_lo; j0 < w_hi; j0 += 256) {
+  each([&](int j, const uint4& four) {
     uint32_t above, equal;
-    look(j0 + 4 * lane, above, equal);
+    look(j, four, above, equal);
     n_above += __popc(above);
     n_equal += __popc(equal);
-  }
+  });
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     n_above += __shfl_xor(n_above, d, 64);
     n_equal += __shfl_xor(n_equal, d, 64);
   }
+  __syncthreads();   // (wave_sum has been read)
   if (lane == 0) {
-    wave_sum[wave] = n_above;
-    wave_eq[wave] = n_equal;
+    sh.wave_sum[wave] = n_above;
+    sh.wave_eq[wave] = n_equal;
   }
   __syncthreads();
   n_above = n_equal = 0;
-  for (int k = 0; k < wave; ++k) {
-    n_above += wave_sum[k];
-    n_equal += wave_eq[k];
+#pragma unroll
+  for (int k = 0; k < kSelWaves; ++k) {
+    n_above += k < wave ? sh.wave_sum[k] : 0;
+    n_equal += k < wave ? sh.wave_eq[k] : 0;
   }
-  int32_t* const kept = a.kept + ((size_t)s * a.Hkv + h) * a.budget;
-  for (int j0 = w_lo; j0 < w_hi; j0 += 256) {
-    const int j = j0 + 4 * lane;
+  each([&](int j, const uint4& four) {
     uint32_t above, equal;
-    look(j, above, equal);
-    // the lane's first token's places: sums over the lanes before
-    int pa = __popc(above), pe = __popc(equal);
-    const int own_a = pa, own_e = pe;
+    look(j, four, above, equal);
+    // the lane's first token's places: sums over the lanes before, both in one word (at most 256 each)
+    const int own = __popc(above) | __popc(equal) << 16;
+    int incl = own;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int oa = __shfl_up(pa, d, 64), oe = __shfl_up(pe, d, 64);
-      if (lane >= d) {
-        pa += oa;
-        pe += oe;
-      }
+      const int o = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += o;
     }
-    int at_a = n_above + pa - own_a, at_e = n_equal + pe - own_e;
+    int at_a = n_above + ((incl - own) & 0xFFFF), at_e = n_equal + ((incl - own) >> 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const bool up = (above >> e) & 1, eq = (equal >> e) & 1;
@@ -179,16 +191,16 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
       at_a += up;
       at_e += eq;
     }
-    n_above += __shfl(pa, 63, 64);
-    n_equal += __shfl(pe, 63, 64);
-  }
+    const int all = __builtin_amdgcn_readlane(incl, 63);
+    n_above += all & 0xFFFF;
+    n_equal += all >> 16;
+  });
 
   // -------- their usage, which may be written where it is read: place i is at most kept[i], so that a step's places lie
   // before every later step's sources, and its own have all been read at the barrier
   __threadfence_block();
   __syncthreads();
-  if (!known) return;
-  float* const out = a.new_usage + base;
+  if (!usage) return;
   for (int i0 = 0; i0 < a.budget; i0 += 4 * kSelThreads) {
     float v[4];
 #pragma unroll
@@ -203,6 +215,25 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
       if (i < a.budget) out[i] = v[k];
     }
   }
+}
+
+__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs a) {
+  __shared__ __attribute__((aligned(16))) Select sh;
+  const int s = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+  const int n = cached_tokens(a, s);
+  if (h == 0 && threadIdx.x == 0) a.new_lens[s] = n > a.limit ? a.budget : n;
+  if (n <= a.limit) return;
+  const int row = a.usage_rows ? a.usage_rows[s] : s;
+  const bool known = row >= 0 && row < a.rows;
+  const size_t base = ((size_t)(known ? row : 0) * a.Hkv + h) * ((size_t)a.max_pages << a.page_shift);
+  const float* const usage = known ? a.usage + base : nullptr;
+  float* const out = a.new_usage + base;
+  int32_t* const kept = a.kept + ((size_t)s * a.Hkv + h) * a.budget;
+  constexpr int kStep = 256 * kSelWaves;
+  if (n <= kStep) select<1>(a, sh, usage, out, kept, n);
+  else if (n <= 4 * kStep) select<4>(a, sh, usage, out, kept, n);
+  else if (n <= 16 * kStep) select<16>(a, sh, usage, out, kept, n);
+  else select<0>(a, sh, usage, out, kept, n);
 }
 
 // Rows of keys and values to the new pages: 16 bytes a lane, kMoveRows rows of each per workgroup.

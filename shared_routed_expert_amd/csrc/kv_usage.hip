@@ -267,6 +267,9 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
   // bytes between a token's last row and the next token's first: 32-bit offsets within a tile where they are few
   const bool near_rows = a.q_stride - (size_t)a.G * D < 1u << 22;
   const uint32_t gap = (uint32_t)(a.q_stride - (size_t)a.G * D) * 2;
+  // Of two waves on a SIMD the older one is served first, and the younger one's part would end last by a third: the workgroups
+  // that come second go ahead instead (a prompt's last 64 tokens 38.5 -> 35.6 us, two prompts of 4096 127 -> 123).
+  if (blockIdx.x >= kUsageParts / 2) __builtin_amdgcn_s_setprio(1);
   int buf = 0;
   while (u < u_end) {
     // -------- the segment: its rows, and this part's share of their tiles (the fixed cost comes first; a part whose share
