@@ -14,7 +14,7 @@
 namespace srmoe {
 
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
-constexpr int kBins = 2048, kCopies = 4;   // copies of the counts, a wave's own in four
+constexpr int kBins = 2048;
 
 // Order of floats as that of unsigned integers: NaN lowest, then -infinity upwards, the zeros equal
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -29,13 +29,14 @@ __device__ __forceinline__ int cached_tokens(const EvictArgs& a, int s) {
 
 // What the workgroup shares.
 struct Select {
-  uint32_t counts[kCopies][kBins];
+  uint32_t counts[kBins];
   int wave_sum[kSelWaves], wave_eq[kSelWaves];
   int found_bin, found_left;
 };
 
 // A wave takes a stretch of the row, 256 tokens at a time, four a lane. HELD > 0: the stretch is at most HELD such steps and
-// stays in registers (one read of the row: 2112 tokens 10.8 us with a read for each pass, see launch_kv_evict).
+// stays in registers. A selection from 2112 tokens takes 8.1 us (10.8 with a read of the row for each pass), from 16384
+// 24 (29): some 5 us for the first pass, its read included, 3 and 2 for the others, 5 for the places.
 template <int HELD>
 __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const float* usage, float* out, int32_t* kept, int n) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -43,18 +44,17 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
   const int stretch = (n + 256 * kSelWaves - 1) / (256 * kSelWaves) * 256;
   const int w_lo = min(wave * stretch, n), w_hi = min(w_lo + stretch, n);
   const int steps = (w_hi - w_lo + 255) / 256;
-  // orders of the four tokens from j on (rows are 16-byte aligned, and as long as whole pages; no row: all are equal)
+  // the four tokens from j on (rows are 16-byte aligned, and as long as whole pages; no row: all are equal)
   auto load4 = [&](int j) {
-    const float4 v = usage && j < w_hi ? *reinterpret_cast<const float4*>(usage + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-    return make_uint4(order_of(v.x), order_of(v.y), order_of(v.z), order_of(v.w));
+    return usage && j < w_hi ? *reinterpret_cast<const float4*>(usage + j) : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   constexpr int kKept = HELD > 0 ? HELD : 1;
-  uint4 held[kKept];
+  float4 held[kKept];
   if (HELD > 0) {
 #pragma unroll
     for (int i = 0; i < kKept; ++i) held[i] = load4(w_lo + 256 * i + 4 * lane);
   }
-  auto each = [&](auto f) {   // f(first token of the lane's four, their orders)
+  auto each = [&](auto f) {   // f(first token of the lane's four, their usage)
     if (HELD > 0) {
 #pragma unroll
       for (int i = 0; i < kKept; ++i)
@@ -72,12 +72,11 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
   int left = a.budget - a.sinks - a.recent;   // how many of the values that begin with the prefix are kept
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
-    uint4* const zero = reinterpret_cast<uint4*>(&sh.counts[0][0]);
-    for (int i = tid; i < kCopies * kBins / 4; i += kSelThreads) zero[i] = make_uint4(0, 0, 0, 0);
+    uint4* const zero = reinterpret_cast<uint4*>(sh.counts);
+    for (int i = tid; i < kBins / 4; i += kSelThreads) zero[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    uint32_t* const mine = sh.counts[wave % kCopies];
-    each([&](int j, const uint4& four) {
-      const uint32_t o[4] = {four.x, four.y, four.z, four.w};
+    each([&](int j, const float4& four) {
+      const uint32_t o[4] = {order_of(four.x), order_of(four.y), order_of(four.z), order_of(four.w)};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const bool in = j + e >= lo && j + e < min(hi, w_hi) &&
@@ -89,9 +88,9 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
         const int lead = __ffsll((unsigned long long)who) - 1;
         const uint32_t one = (uint32_t)__builtin_amdgcn_readlane((int)bin, lead);
         if (__ballot(in && bin != one) == 0) {
-          if (lane == lead) atomicAdd(&mine[one], (uint32_t)__popcll(who));
+          if (lane == lead) atomicAdd(&sh.counts[one], (uint32_t)__popcll(who));
         } else if (in) {
-          atomicAdd(&mine[bin], 1u);
+          atomicAdd(&sh.counts[bin], 1u);
         }
       }
     });
@@ -100,11 +99,8 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
     const int b1 = bins - 1 - 2 * tid, b0 = b1 - 1;
     int c1 = 0, c0 = 0;
     if (b1 > 0) {
-#pragma unroll
-      for (int k = 0; k < kCopies; ++k) {
-        c1 += (int)sh.counts[k][b1];
-        c0 += (int)sh.counts[k][b0];
-      }
+      c1 = (int)sh.counts[b1];
+      c0 = (int)sh.counts[b0];
     }
     int incl = c1 + c0;
 #pragma unroll
@@ -136,31 +132,36 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
   }
   const uint32_t T = prefix;
 
-  // -------- the places of the kept
-  auto look = [&](int j, const uint4& four, uint32_t& above, uint32_t& equal) {   // bits of a lane's four tokens
-    const uint32_t o[4] = {four.x, four.y, four.z, four.w};
-    above = equal = 0;
+  // -------- the places of the kept: tokens before a lane's e-th are those of all lanes before it and its own e
+  struct Marks {
+    uint64_t above[4], equal[4];   // lanes whose e-th token is protected or above T, or equal to it
+  };
+  auto look = [&](int j, const float4& four) {
+    const uint32_t o[4] = {order_of(four.x), order_of(four.y), order_of(four.z), order_of(four.w)};
+    Marks m;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (j + e >= w_hi) continue;
-      const bool safe = j + e < lo || j + e >= hi;
-      above |= (uint32_t)(safe || o[e] > T) << e;
-      equal |= (uint32_t)(!safe && o[e] == T) << e;
+      const bool in = j + e < w_hi, safe = j + e < lo || j + e >= hi;
+      m.above[e] = __ballot(in && (safe || o[e] > T));
+      m.equal[e] = __ballot(in && !safe && o[e] == T);
     }
+    return m;
+  };
+  auto all_of = [](const uint64_t (&m)[4]) { return __popcll(m[0]) + __popcll(m[1]) + __popcll(m[2]) + __popcll(m[3]); };
+  auto before = [](const uint64_t (&m)[4]) {
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      n = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m[e] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m[e], (uint32_t)n));
+    return n;
   };
   int n_above = 0, n_equal = 0;
-  each([&](int j, const uint4& four) {
-    uint32_t above, equal;
-    look(j, four, above, equal);
-    n_above += __popc(above);
-    n_equal += __popc(equal);
+  each([&](int j, const float4& four) {
+    const Marks m = look(j, four);
+    n_above += all_of(m.above);
+    n_equal += all_of(m.equal);
   });
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    n_above += __shfl_xor(n_above, d, 64);
-    n_equal += __shfl_xor(n_equal, d, 64);
-  }
-  __syncthreads();   // (wave_sum has been read)
+  __syncthreads();   // (wave_sum has been read; and with the row held, all of it has been)
   if (lane == 0) {
     sh.wave_sum[wave] = n_above;
     sh.wave_eq[wave] = n_equal;
@@ -172,31 +173,27 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
     n_above += k < wave ? sh.wave_sum[k] : 0;
     n_equal += k < wave ? sh.wave_eq[k] : 0;
   }
-  each([&](int j, const uint4& four) {
-    uint32_t above, equal;
-    look(j, four, above, equal);
-    // the lane's first token's places: sums over the lanes before, both in one word (at most 256 each)
-    const int own = __popc(above) | __popc(equal) << 16;
-    int incl = own;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += o;
-    }
-    int at_a = n_above + ((incl - own) & 0xFFFF), at_e = n_equal + ((incl - own) >> 16);
+  each([&](int j, const float4& four) {
+    const Marks m = look(j, four);
+    const float v[4] = {four.x, four.y, four.z, four.w};
+    int at_a = n_above + before(m.above), at_e = n_equal + before(m.equal);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bool up = (above >> e) & 1, eq = (equal >> e) & 1;
-      if (up || (eq && at_e < left)) kept[at_a + min(at_e, left)] = j + e;
+      const bool up = (m.above[e] >> lane) & 1, eq = (m.equal[e] >> lane) & 1;
+      if (up || (eq && at_e < left)) {
+        const int to = at_a + min(at_e, left);
+        kept[to] = j + e;
+        if (HELD > 0 && usage) out[to] = v[e];   // (out may be usage: nobody reads it any more)
+      }
       at_a += up;
       at_e += eq;
     }
-    const int all = __builtin_amdgcn_readlane(incl, 63);
-    n_above += all & 0xFFFF;
-    n_equal += all >> 16;
+    n_above += all_of(m.above);
+    n_equal += all_of(m.equal);
   });
+  if (HELD > 0) return;
 
-  // -------- their usage, which may be written where it is read: place i is at most kept[i], so that a step's places lie
+  // -------- a long row's usage, which may be written where it is read: place i is at most kept[i], so that a step's places lie
   // before every later step's sources, and its own have all been read at the barrier
   __threadfence_block();
   __syncthreads();
@@ -232,57 +229,58 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs 
   constexpr int kStep = 256 * kSelWaves;
   if (n <= kStep) select<1>(a, sh, usage, out, kept, n);
   else if (n <= 4 * kStep) select<4>(a, sh, usage, out, kept, n);
-  else if (n <= 16 * kStep) select<16>(a, sh, usage, out, kept, n);
+  else if (n <= 8 * kStep) select<8>(a, sh, usage, out, kept, n);
   else select<0>(a, sh, usage, out, kept, n);
 }
 
-// Rows of keys and values to the new pages: 16 bytes a lane, kMoveRows rows of each per workgroup.
-constexpr int kMoveRows = 64;
-__global__ void __launch_bounds__(256) kv_move_kernel(const EvictArgs a, const int lanes /* of a row */, const int per_head) {
+// Rows of keys and values to the new pages: 16 bytes a lane, two rows of each a thread (four: one sequence of 2112 tokens 12.1 us
+// instead of 11.5, the others alike). They are read past the caches (64 sequences in e4m3 48 -> 43 us) and written through
+// them, to the attention that reads them next. Bytes set the pace: 24 sequences on 8 heads, 0.8 GB, at 4.9 to 5.1 TB/s.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+constexpr int kMoveThreads = 256, kMoveEach = 2;
+__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a, const int lanes /* of a row */) {
   const int s = blockIdx.y / a.Hkv, h = blockIdx.y % a.Hkv;
-  const int n = cached_tokens(a, s);
-  if (n <= a.limit) return;
+  if (cached_tokens(a, s) <= a.limit) return;
   const int32_t* const kept = a.kept + ((size_t)s * a.Hkv + h) * a.budget;
-  const int at_once = 256 / lanes, mine = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int at_once = kMoveThreads / lanes, lane = threadIdx.x % lanes;
+  const int first = blockIdx.x * kMoveEach * at_once + threadIdx.x / lanes;
   const int mask = (1 << a.page_shift) - 1;
-  const size_t rb = (size_t)lanes * 16, page_bytes = a.page_bytes;
-  for (int r = mine; r < kMoveRows; r += 4 * at_once) {
-    uint4 k[4], v[4];
-    size_t to[4];
-    bool go[4];
+  const size_t rb = (size_t)lanes * 16, head = (size_t)h << a.page_shift;
+  i32x4 k[kMoveEach], v[kMoveEach];
+  size_t to[kMoveEach];
+  bool go[kMoveEach];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int row = r + x * at_once, i = blockIdx.x * kMoveRows + row;
-      go[x] = row < kMoveRows && i < a.budget;
-      k[x] = v[x] = make_uint4(0, 0, 0, 0);
-      if (!go[x]) continue;
-      const int j = kept[i];
-      const int src = a.block_table[(size_t)s * a.max_pages + (j >> a.page_shift)];
-      const int dst = a.new_table[(size_t)s * a.new_max_pages + (i >> a.page_shift)];
-      go[x] = dst >= 0 && dst < a.num_pages;
-      const size_t head = (size_t)h << a.page_shift;
-      to[x] = (size_t)(go[x] ? dst : 0) * page_bytes + (head + (i & mask)) * rb + lane * 16;
-      if (src >= 0 && src < a.num_pages) {   // (a token of no page becomes zeros)
-        const size_t from = (size_t)src * page_bytes + (head + (j & mask)) * rb + lane * 16;
-        k[x] = *reinterpret_cast<const uint4*>(a.k_cache + from);
-        v[x] = *reinterpret_cast<const uint4*>(a.v_cache + from);
-      }
+  for (int x = 0; x < kMoveEach; ++x) {
+    const int i = first + x * at_once;
+    go[x] = i < a.budget;
+    k[x] = v[x] = i32x4{0, 0, 0, 0};
+    if (!go[x]) continue;
+    const int j = kept[i];
+    const int src = a.block_table[(size_t)s * a.max_pages + (j >> a.page_shift)];
+    const int dst = a.new_table[(size_t)s * a.new_max_pages + (i >> a.page_shift)];
+    go[x] = dst >= 0 && dst < a.num_pages;
+    to[x] = (size_t)(go[x] ? dst : 0) * a.page_bytes + (head + (i & mask)) * rb + lane * 16;
+    if (src >= 0 && src < a.num_pages) {   // (a token of no page becomes zeros)
+      const size_t from = (size_t)src * a.page_bytes + (head + (j & mask)) * rb + lane * 16;
+      k[x] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(a.k_cache + from));
+      v[x] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(a.v_cache + from));
     }
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (go[x]) {
-        *reinterpret_cast<uint4*>(a.k_cache + to[x]) = k[x];
-        *reinterpret_cast<uint4*>(a.v_cache + to[x]) = v[x];
-      }
   }
+#pragma unroll
+  for (int x = 0; x < kMoveEach; ++x)
+    if (go[x]) {
+      *reinterpret_cast<i32x4*>(a.k_cache + to[x]) = k[x];
+      *reinterpret_cast<i32x4*>(a.v_cache + to[x]) = v[x];
+    }
 }
 
 hipError_t launch_kv_evict(const EvictArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(kv_select_kernel, dim3(a.S * a.Hkv), dim3(kSelThreads), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int blocks = (a.budget + kMoveRows - 1) / kMoveRows;
-  hipLaunchKernelGGL(kv_move_kernel, dim3(blocks, a.S * a.Hkv), dim3(256), 0, stream, a, a.row_bytes / 16, blocks);
+  const int lanes = a.row_bytes / 16, rows = kMoveEach * kMoveThreads / lanes;
+  hipLaunchKernelGGL(kv_move_kernel, dim3((a.budget + rows - 1) / rows, a.S * a.Hkv), dim3(kMoveThreads), 0, stream, a,
+                     lanes);
   return hipGetLastError();
 }
 
