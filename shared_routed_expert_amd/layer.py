@@ -164,22 +164,26 @@ class FusedMoE:
         if x is None or weight is None or weight.dtype != torch.float32 or tuple(weight.shape) != (H,) \
                 or not weight.is_contiguous() or weight.device != self.out.device:
             raise ValueError(f"weight is float32 [{H}] on {self.out.device}")
+        if self.out.device.type != "cuda":
+            raise ValueError("the layer is not on a GPU")
         if residual is not None and residual_out is None:
             residual_out = torch.empty_like(residual)
         if y is None:
             y = torch.empty((T, H), dtype=torch.bfloat16, device=self.out.device)
         base = self.ws.data_ptr()
-        L.moe_add_rms_norm(x, x.stride(0) if T > 1 else H, residual, residual_out, weight, eps, T, H, self.scale_mode, y,
-                           base + self.offsets["xq"], base + self.offsets["sx"], stream)
+        with torch.cuda.device(self.out.device):
+            L.moe_add_rms_norm(x, x.stride(0) if T > 1 else H, residual, residual_out, weight, eps, T, H, self.scale_mode, y,
+                               base + self.offsets["xq"], base + self.offsets["sx"], stream)
         return y, residual_out
 
     def experts_normed(self, W: DeviceWeights, stream=None):
         """The experts on what add_norm left in the workspace, by the routing tables of route and align (or of
         forward_normed): moe_fused_ffn without its quantisation of x, then the combine."""
         T, H, I, E1, K1, bm = self.dims()
-        L.moe_ffn_experts(W.w13, W.s13, W.w2, W.s2, self.scale_mode, T, H, I, E1, K1, bm, self.sorted_slot_ids,
-                          self.block_expert, self.num_padded, self.topk_w, self.ws, self.ws_bytes, stream)
-        self.combine(stream)
+        with torch.cuda.device(self.out.device):
+            L.moe_ffn_experts(W.w13, W.s13, W.w2, W.s2, self.scale_mode, T, H, I, E1, K1, bm, self.sorted_slot_ids,
+                              self.block_expert, self.num_padded, self.topk_w, self.ws, self.ws_bytes, stream)
+            self.combine(stream)
         return self.out
 
     def forward_normed(self, x, norm_w, w_router, bias, W: DeviceWeights, residual=None, eps=1e-5, residual_out=None,
@@ -188,9 +192,10 @@ class FusedMoE:
         codes. Returns (out, residual_out)."""
         y, h = self.add_norm(x, norm_w, residual, eps, residual_out, stream=stream)
         self._router_ws()
-        L.moe_route_from_x(y, w_router, bias, self.T, self.H, self.E, self.K, shared_weight, self.topk_ids, self.topk_w,
-                           self.router_ws, self.router_ws_bytes, stream)
-        self.align(stream)
+        with torch.cuda.device(self.out.device):
+            L.moe_route_from_x(y, w_router, bias, self.T, self.H, self.E, self.K, shared_weight, self.topk_ids, self.topk_w,
+                               self.router_ws, self.router_ws_bytes, stream)
+            self.align(stream)
         return self.experts_normed(W, stream), h
 
     # views into the workspace, for inspecting the stages

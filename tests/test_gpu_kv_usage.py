@@ -82,7 +82,7 @@ def check(c, usage, lse, sees, scale, cap, prev=None, decay=1.0, rows=None, max_
         assert np.all(err <= bar), (s, np.argwhere(~(err <= bar))[:3], float(np.max(err / np.maximum(bar, 1e-300))))
         worst = max(worst, float(np.max(err / np.maximum(bar, 1e-300), initial=0)))
         want_guard[row, :, :kv] = False
-    assert np.array_equal(usage[want_guard], guard[want_guard])
+    assert np.array_equal(usage[want_guard], guard[want_guard], equal_nan=True)
     return worst
 
 
@@ -293,3 +293,43 @@ def test_graph_replays_match_eager(n):
         d.call()
         torch.cuda.synchronize()
         assert np.array_equal(d.usage.cpu().numpy(), eager[i])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(12, 1, 128), (16, 4, 64), (8, 1, 256)])
+def test_rows_far_apart(Hq, Hkv, D):
+    """q_stride of more than 2^22 values: the rows' places within a tile no longer fit 32 bits."""
+    c = make_case([11, 5], [300, 40], Hq, Hkv, D, 16, False, seed=20)
+    sees = [oracle.visible_prefill(n, k, 0) for n, k in zip(c.ns, c.kvs)]
+    lse = some_lse(c, sees)
+    d = UseDev(c, lse)
+    stride = (1 << 22) + Hq * D + 8
+    far = torch.full((c.T, stride), 0x7FC1, dtype=torch.int16, device=DEV)
+    far[:, :Hq * D] = d.q
+    d.q = far
+    note(f"usage, rows {stride} values apart")
+    L.moe_kv_usage(far, stride, d.kv[:, 0], L.KV_BF16, None, c.kv.shape[0], c.page, d.kv.stride(0), d.table, c.table.shape[1],
+                   d.cu, d.kvl, None, d.lse, 2, c.T, d.max_q, Hq, Hkv, D, D ** -0.5, 0.0, None, 1.0, d.usage, None, 2, d.ws,
+                   d.ws_bytes)
+    torch.cuda.synchronize()
+    check(c, d.usage.cpu().numpy(), lse, sees, D ** -0.5, 0.0)
+
+
+def test_two_streams_with_their_own_workspaces():
+    devs = []
+    for seed, ns, kvs in ((1, [70, 5], [900, 30]), (2, [200, 1], [200, 2000]), (3, [1, 2], [5000, 9])):
+        c = make_case(ns, kvs, 12, 1, 128, 16, False, seed=seed)
+        devs.append(UseDev(c, some_lse(c, [oracle.visible_prefill(n, k, 0) for n, k in zip(ns, kvs)])))
+    want = []
+    for d in devs:
+        d.call()
+        torch.cuda.synchronize()
+        want.append(d.usage.clone())
+        d.usage.fill_(GUARD)
+    streams = [torch.cuda.Stream() for _ in devs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for d, s in zip(devs, streams):
+            d.call(stream=s)
+    torch.cuda.synchronize()
+    for d, w in zip(devs, want):
+        assert torch.equal(d.usage, w)

@@ -243,3 +243,68 @@ def test_cache_object():
     out = cache.window_attention(q, up(c.table), up(c.cu_q), up(np.array(c.kvs, np.int32)), 20, 64, 4, lse=lse)
     torch.cuda.synchronize()
     check(c, bits_of(out.view(torch.int16)), lse.cpu().numpy(), sees_of(c, 64, 4), 128 ** -0.5, 0.0, guard=0)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_many_row_tiles_under_a_window_of_thousands(wide):
+    """Thousands of segments of more than 4096 keys (the kernel looks at the lengths before it takes them whole): some of the
+    tokens against the oracle."""
+    n, kv, window = 3200, 6000, 4500
+    c = make_case([n, 1], [kv, 100], 64, 1, 64, 64, False, seed=31)
+    if wide:
+        t = np.full((2, 131072 // c.page), 1 << 30, np.int32)
+        t[:, :c.table.shape[1]] = c.table
+        c.table = t
+    d = WinDev(c)
+    note(f"window {window}, {n} tokens of 64 heads, wide={wide}")
+    d.run(window, 9)
+    torch.cuda.synchronize()
+    out, lse = bits_of(d.out), d.lse.cpu().numpy()
+    rows = np.unique(np.concatenate([np.arange(0, n, 173), [1, 2, 3, n - 2, n - 1], np.arange(1500, 1520)]))
+    see = oracle.visible_window(n, kv, window, 9)[rows]
+    e = make_case([len(rows)], [kv], 64, 1, 64, 64, False, seed=31)
+    e.q, e.k, e.v, e.T = c.q[rows], c.k[:1], c.v[:1], len(rows)
+    check(e, out[rows], lse[rows], [see], 64 ** -0.5, 0.0)
+
+
+def test_pages_that_the_window_leaves_are_given_away():
+    """Decoding with a pool of few pages: each step appends a token, and a page that no later token will see goes back to
+    the pool, from which the other sequence takes it; the attention against all that was ever appended."""
+    Hq, Hkv, D, page, window, sinks = 8, 2, 64, 16, 40, 5
+    rng = np.random.default_rng(2)
+    cache = PagedKVCache(12, page, Hkv, D, device=DEV)
+    cache.kv.view(torch.int16).fill_(0x7FC1)
+    free = [int(x) for x in rng.permutation(12)]
+    table = np.full((2, 16), -1, np.int32)
+    owned = [[False] * 16 for _ in range(2)]
+    k, v = [[], []], [[], []]
+    for step in range(150):
+        lens = [step + 1, step // 2 + 1]
+        active = [0, 1] if step % 2 == 0 else [0]
+        slots = []
+        for s in active:
+            at = lens[s] - 1
+            if at % page == 0:
+                table[s, at // page] = free.pop()
+                owned[s][at // page] = True
+            slots.append(int(table[s, at // page]) * page + at % page)
+        qkv = torch.from_numpy(rng.standard_normal((len(active), (Hq + 2 * Hkv) * D)).astype(np.float32)).to(DEV).bfloat16()
+        q = cache.append(qkv, Hq, up(np.array(slots, np.int32)))
+        new = qkv.double().cpu().numpy().reshape(len(active), Hq + 2 * Hkv, D)
+        for i, s in enumerate(active):
+            k[s].append(new[i, Hq:Hq + Hkv])
+            v[s].append(new[i, Hq + Hkv:])
+        lse = torch.empty((len(active), Hq), device=DEV)
+        out = cache.window_attention(q, up(table[active]), up(np.arange(len(active) + 1, dtype=np.int32)),
+                                     up(np.array([lens[s] for s in active], np.int32)), 1, window, sinks, lse=lse)
+        torch.cuda.synchronize()
+        c = make_case([1] * len(active), [lens[s] for s in active], Hq, Hkv, D, page, False, 0)
+        c.q, c.T = bits_of(q.view(torch.int16)).reshape(len(active), -1), len(active)
+        c.k, c.v = [np.array(k[s]) for s in active], [np.array(v[s]) for s in active]
+        check(c, bits_of(out.view(torch.int16)), lse.cpu().numpy(), sees_of(c, window, sinks), D ** -0.5, 0.0)
+        for s in active:   # the next token sees from lens + 1 - window on
+            for p in range(16):
+                if owned[s][p] and p * page >= sinks and (p + 1) * page <= lens[s] + 1 - window:
+                    free.append(int(table[s, p]))
+                    owned[s][p] = False
+                    table[s, p] = rng.choice([-1, 1 << 30, int(rng.integers(0, 12))])

@@ -61,3 +61,5 @@ def test_layer_object_rejects():
                 dict(weight=None)):
         with pytest.raises(ValueError):
             m.add_norm(**{**dict(x=x, weight=w), **bad})
+    with pytest.raises(ValueError, match="not on a GPU"):
+        m.add_norm(x, w)
