@@ -54,6 +54,79 @@ struct alignas(32) UsageDesc {
 
 constexpr int kUsageParts = 512;   // two workgroups on each CU
 
+// All sequences' costs laid end to end: up to 64 of them one per lane, in every wave by itself; more, a stretch of them per
+// thread of the workgroup (and barriers).
+struct Line {
+  SeqBlocks own;        // of this lane's sequence, S <= 64
+  int s_lo, s_hi;
+  long total, before, mine;
+};
+__device__ __forceinline__ SeqBlocks uniform(SeqBlocks t) {
+  t.row0 = uni(t.row0); t.n = uni(t.n); t.kv = uni(t.kv); t.ctx = uni(t.ctx); t.all = uni(t.all); t.MB = uni(t.MB);
+  return t;
+}
+template <class F>   // cost(SeqBlocks) of a sequence
+__device__ __forceinline__ Line lay_line(const AttnArgs& a, int KB, F cost, long* scan_sum /* LDS, 4 */) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  Line l{};
+  const bool few = a.S <= 64;
+  const int per = few ? 1 : (a.S + 255) / 256;
+  l.s_lo = min((few ? lane : tid) * per, a.S);
+  l.s_hi = min(l.s_lo + per, a.S);
+  for (int s = l.s_lo; s < l.s_hi; ++s) {
+    l.own = seq_blocks(a, s, KB);
+    l.mine += cost(l.own);
+  }
+  long incl = l.mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const long o = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += o;
+  }
+  l.before = incl - l.mine;
+  if (few) {
+    l.total = read_lane(incl, 63);
+    return l;
+  }
+  if (lane == 63) scan_sum[tid >> 6] = incl;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < tid >> 6) l.before += scan_sum[i];
+    l.total += scan_sum[i];
+  }
+  l.total = uni(l.total);
+  return l;
+}
+// The sequence in which `unit` lies, and how far into it; S <= 64: for this wave, else the one thread that knows writes it
+struct Place {
+  int s;
+  long rem;
+};
+__device__ __forceinline__ Place place_few(const Line& l, long unit, SeqBlocks& seq) {
+  const int s = __ffsll((unsigned long long)__ballot(l.mine > 0 && unit >= l.before && unit < l.before + l.mine)) - 1;
+  seq.row0 = __builtin_amdgcn_readlane(l.own.row0, s);
+  seq.n = __builtin_amdgcn_readlane(l.own.n, s);
+  seq.kv = __builtin_amdgcn_readlane(l.own.kv, s);
+  seq.ctx = __builtin_amdgcn_readlane(l.own.ctx, s);
+  seq.all = __builtin_amdgcn_readlane(l.own.all, s);
+  seq.MB = __builtin_amdgcn_readlane(l.own.MB, s);
+  return {s, unit - read_lane(l.before, s)};
+}
+template <class F>
+__device__ __forceinline__ void place_many(const AttnArgs& a, const Line& l, int KB, F cost, long unit, Place* to) {
+  if (!(l.mine > 0 && unit >= l.before && unit < l.before + l.mine)) return;
+  long r = unit - l.before;
+  for (int s = l.s_lo; s < l.s_hi; ++s) {
+    const long c = cost(seq_blocks(a, s, KB));
+    if (r < c) {
+      *to = {s, r};
+      return;
+    }
+    r -= c;
+  }
+}
+
 // Where a sequence's weights are, or null: they are not kept
 __device__ __forceinline__ size_t usage_at(const UsageArgs& u, int s, int head, bool* kept) {
   const int row = u.usage_rows ? u.usage_rows[s] : s;
@@ -183,34 +256,13 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
   extern __shared__ __attribute__((aligned(1024))) uint16_t qs[];   // two tiles
   __shared__ float row_l2[2][C::ROWS], row_fix[2][C::ROWS];
   __shared__ long scan_sum[C::kWaves];
-  __shared__ long found_rem;
-  __shared__ int found_s;
-  __shared__ SeqBlocks found_seq;
+  __shared__ Place found;
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-  // -------- which part of the line of segments is this workgroup's: a stretch of sequences per thread
-  const int per = (a.S + C::kThreads - 1) / C::kThreads;
-  const int s_lo = min(tid * per, a.S), s_hi = min(s_lo + per, a.S);
-  long mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) {
-    const SeqBlocks t = seq_blocks(a, s, C::KB);
-    mine += t.cost(t.MB, C::KB, a.G, C::kSegCost) * a.Hkv;
-  }
-  long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const long o = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 63) scan_sum[wave] = incl;
-  __syncthreads();
-  long total = 0, before = incl - mine;
-#pragma unroll
-  for (int i = 0; i < C::kWaves; ++i) {
-    if (i < wave) before += scan_sum[i];
-    total += scan_sum[i];
-  }
-  total = uni(total);
+  // -------- which part of the line of segments is this workgroup's
+  auto cost = [&](const SeqBlocks& t) { return t.cost(t.MB, C::KB, a.G, C::kSegCost) * a.Hkv; };
+  const Line line = lay_line(a, C::KB, cost, scan_sum);
+  const long total = line.total;
   const int parts = (int)min((long)parts_max, (total + C::kSegCost - 1) / C::kSegCost);
   const int w = xcd_tile((int)blockIdx.x, parts);   // consecutive parts on one XCD: neighbouring keys, the same rows
   // no segment begins in these parts until one is written below
@@ -221,28 +273,18 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
   const Parts split(total, parts);
   long u = split.begin(w);
   const long u_end = split.begin(w + 1);
-  if (mine > 0 && u >= before && u < before + mine) {   // one thread alone
-    long r = u - before;
-    for (int i = s_lo; i < s_hi; ++i) {
-      const SeqBlocks t = seq_blocks(a, i, C::KB);
-      const long cost = t.cost(t.MB, C::KB, a.G, C::kSegCost) * a.Hkv;
-      if (r < cost) {
-        found_s = i;
-        found_seq = t;
-        found_rem = r;
-        break;
-      }
-      r -= cost;
-    }
+  Place at;
+  SeqBlocks seq;
+  if (a.S <= 64) {
+    at = place_few(line, u, seq);
+  } else {
+    place_many(a, line, C::KB, cost, u, &found);
+    __syncthreads();
+    at = {uni(found.s), uni(found.rem)};
+    seq = uniform(seq_blocks(a, at.s, C::KB));
   }
-  __syncthreads();
-  auto uniform = [](SeqBlocks t) {
-    t.row0 = uni(t.row0); t.n = uni(t.n); t.kv = uni(t.kv); t.ctx = uni(t.ctx); t.all = uni(t.all); t.MB = uni(t.MB);
-    return t;
-  };
-  int s = uni(found_s);
-  long rem = uni(found_rem);
-  SeqBlocks seq = uniform(found_seq);
+  int s = at.s;
+  long rem = at.rem;
   int h, kb;
   {
     const long per_head = seq.cost(seq.MB, C::KB, a.G, C::kSegCost);
@@ -293,14 +335,18 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
         const int first = r0 + t * C::ROWS, tok0 = uni(token_of(first)), last = min(C::ROWS, r_end - first) - 1;
         const uint16_t* const q0 = qh + (size_t)tok0 * a.q_stride;
         const int lead = first - tok0 * a.G;   // rows of its first token before the tile
+        auto loads = [&](auto near) {
 #pragma unroll
-        for (int y = 0; y < C::LOADS; ++y) {
-          const int x = y * C::kWaves + wave;   // (rows past the last repeat it)
-          const int at = x * C::RPL + lane / C::CH, r = lead + min(at, last), tok = near_token(r, magic_near);
-          const uint32_t lds = qs_off + b * (C::ROWS * D * 2) + x * 1024, chunk = ((lane % C::CH) ^ swizzle(at)) * 16;
-          if (near_rows) load_lds16_near(lds, __umul24(tok, gap) + r * (2 * D) + chunk, q0);
-          else load_lds16_at(lds, reinterpret_cast<const uint8_t*>(q0 + tok * (a.q_stride - a.G * D) + r * D) + chunk);
-        }
+          for (int y = 0; y < C::LOADS; ++y) {
+            const int x = y * C::kWaves + wave;   // (rows past the last repeat it)
+            const int at = x * C::RPL + lane / C::CH, r = lead + min(at, last), tok = near_token(r, magic_near);
+            const uint32_t lds = qs_off + b * (C::ROWS * D * 2) + x * 1024, chunk = ((lane % C::CH) ^ swizzle(at)) * 16;
+            if (near) load_lds16_near(lds, __umul24(tok, gap) + r * (2 * D) + chunk, q0);
+            else load_lds16_at(lds, reinterpret_cast<const uint8_t*>(q0 + tok * (a.q_stride - a.G * D) + r * D) + chunk);
+          }
+        };
+        if (near_rows) loads(std::true_type{});
+        else loads(std::false_type{});
         if (tid / C::ROWS == t % (C::kThreads / C::ROWS)) {
           const int r = lead + min(tid & (C::ROWS - 1), last), tok = near_token(r, magic_near);
           ahead = args.lse[(size_t)(seq.row0 + tok0 + tok) * a.Hq + h * a.G + r - tok * a.G];
@@ -393,7 +439,7 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
               for (int x = 0; x < C::STEPS; ++x) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a product
                 if (hand_over) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 48 / C::STEPS, 0);
+                if (x > 0) __builtin_amdgcn_sched_group_barrier(0x002, 7, 0);
               }
             }
           }
@@ -478,64 +524,32 @@ __global__ void __launch_bounds__(256, 2) kv_usage_few_kernel(const UsageArgs ar
   extern __shared__ __attribute__((aligned(1024))) uint8_t stages[];
   const AttnArgs& a = args.a;
   __shared__ long scan_sum[4];
-  __shared__ long found_rem[4];
-  __shared__ int found_s[4];
+  __shared__ Place found[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int col = lane & 15, quarter = lane >> 4;
-  const int per = (a.S + 255) / 256;
-  const int s_lo = min(tid * per, a.S), s_hi = min(s_lo + per, a.S);
-  long mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) mine += (long)seq_blocks(a, s, KB).MB * a.Hkv;
-  long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const long o = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 63) scan_sum[wave] = incl;
-  __syncthreads();
-  long total = 0, before = incl - mine;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < wave) before += scan_sum[i];
-    total += scan_sum[i];
-  }
-  total = uni(total);
+  auto cost = [&](const SeqBlocks& t) { return (long)t.MB * a.Hkv; };
+  const Line line = lay_line(a, KB, cost, scan_sum);
   const int block = xcd_tile((int)blockIdx.x, (int)gridDim.x);
-  const Parts split(total, 4 * (int)gridDim.x);
-  // the sequences in which this workgroup's waves begin
+  const Parts split(line.total, 4 * (int)gridDim.x);
+  if (a.S > 64) {   // the sequences in which this workgroup's waves begin
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long u = split.begin(4 * block + i);
-    if (mine > 0 && u >= before && u < before + mine) {
-      long r = u - before;
-      for (int at = s_lo; at < s_hi; ++at) {
-        const long cost = (long)seq_blocks(a, at, KB).MB * a.Hkv;
-        if (r < cost) {
-          found_s[i] = at;
-          found_rem[i] = r;
-          break;
-        }
-        r -= cost;
-      }
-    }
+    for (int i = 0; i < 4; ++i) place_many(a, line, KB, cost, split.begin(4 * block + i), &found[i]);
+    __syncthreads();
   }
-  __syncthreads();
   long u = split.begin(4 * block + wave);
   const long u_end = split.begin(4 * block + wave + 1);
   if (u >= u_end) return;
-  auto uniform = [](SeqBlocks t) {
-    t.row0 = uni(t.row0); t.n = uni(t.n); t.kv = uni(t.kv); t.ctx = uni(t.ctx); t.all = uni(t.all); t.MB = uni(t.MB);
-    return t;
-  };
-  int s = uni(found_s[wave]);
-  SeqBlocks seq = uniform(seq_blocks(a, s, KB));
-  int h, kb;
-  {
-    const long rem = uni(found_rem[wave]);
-    h = uni((int)div_pos(rem, seq.MB));
-    kb = uni((int)(rem - (long)h * seq.MB));
+  Place at;
+  SeqBlocks seq;
+  if (a.S <= 64) {
+    at = place_few(line, u, seq);
+  } else {
+    at = {uni(found[wave].s), uni(found[wave].rem)};
+    seq = uniform(seq_blocks(a, at.s, KB));
   }
+  int s = at.s, h, kb;
+  h = uni((int)div_pos(at.rem, seq.MB));
+  kb = uni((int)(at.rem - (long)h * seq.MB));
   const int page_mask = (1 << a.page_shift) - 1;
   const size_t page_bytes = a.page_stride * (FP8 ? 1 : 2);
   uint8_t* const mine_lds = stages + wave * (F::LDS / 4);
