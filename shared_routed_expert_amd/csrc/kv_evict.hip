@@ -2,9 +2,11 @@
 // `recent`, and the m = budget - sinks - recent of largest usage between them (equal ones: the earlier), in order of position.
 //
 // Selection, one workgroup per sequence and kv head. Usage as an unsigned integer of the same order; the m-th largest is
-// found by three passes over the row (11, 11 and 10 bits, counted in LDS), which say what it is, T, and how many of the
-// values equal to T are kept, r. The place of token j among the kept is then (tokens before j that are protected or above T) +
-// min(r, tokens before j equal to T): counted per wave's stretch of the row, added up, and written out.
+// found by up to three passes over the row (12, 10 and 10 bits, counted in LDS), which say what it is, T, and how many of the
+// values equal to T are kept, r; they end where all values of a prefix are kept. The place of token j among the kept is then
+// (tokens before j that are protected or above T) + min(r, tokens before j equal to T): counted per wave's stretch of the row,
+// added up, and written out. Bound by one CU's vector unit and its counting in LDS, not by bytes. (11, 11 and 10 bits: 0.5 us
+// more in 16384 tokens, since usage crowds a few bins.)
 //
 // The kept tokens' keys and values then go to the sequence's new pages, which no sequence reads in this call: every row is read
 // once and written once, by any workgroup at any time, and pages that other sequences share are left whole.
@@ -14,32 +16,37 @@
 namespace srmoe {
 
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
-constexpr int kBins = 2048;
+constexpr int kBins = 4096 + 2 * 1024;   // of passes over 12, 10 and 10 bits
 
 // Order of floats as that of unsigned integers: NaN lowest, then -infinity upwards, the zeros equal
 __device__ __forceinline__ uint32_t order_of(float v) {
-  if (v != v) return 0u;
   const uint32_t b = __float_as_uint(v + 0.0f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t o = b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+  return v != v ? 0u : o;
 }
 
 __device__ __forceinline__ int cached_tokens(const EvictArgs& a, int s) {
   return min(max(a.kv_lens[s], 0), a.max_pages << a.page_shift);
 }
 
-// What the workgroup shares.
+// A token as the selection sees it: protected ones above all orders, those past the end among the lowest (they come last of
+// their equals, so none is kept)
+constexpr uint32_t kProtected = 0xFFFFFFFFu, kTop = 0xFF800000u /* +infinity */;
+
+// What the workgroup shares: the bins of every pass, cleared together.
 struct Select {
   uint32_t counts[kBins];
   int wave_sum[kSelWaves], wave_eq[kSelWaves];
-  int found_bin, found_left;
+  int found_bin, found_left, found_count;
 };
 
 // A wave takes a stretch of the row, 256 tokens at a time, four a lane. HELD > 0: the stretch is at most HELD such steps and
-// stays in registers. A selection from 2112 tokens takes 8.1 us (10.8 with a read of the row for each pass), from 16384
-// 24 (29): some 5 us for the first pass, its read included, 3 and 2 for the others, 5 for the places.
+// stays in registers, usage and order (16 steps spill); else each pass reads it again, four loads in flight. A cut of one
+// sequence of 2112 tokens takes 11 to 12 us, of 32768 26, of 131072 76 (112 with each token's place compared in every
+// pass), the move included.
 template <int HELD>
 __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const float* usage, float* out, int32_t* kept, int n) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lo = a.sinks, hi = n - a.recent;   // those that are chosen among
   const int stretch = (n + 256 * kSelWaves - 1) / (256 * kSelWaves) * 256;
   const int w_lo = min(wave * stretch, n), w_hi = min(w_lo + stretch, n);
@@ -48,39 +55,64 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
   auto load4 = [&](int j) {
     return usage && j < w_hi ? *reinterpret_cast<const float4*>(usage + j) : make_float4(0.f, 0.f, 0.f, 0.f);
   };
+  auto orders = [&](int j0, const float4& v) {   // of the 256 tokens from j0 on
+    uint4 o = make_uint4(order_of(v.x), order_of(v.y), order_of(v.z), order_of(v.w));
+    if (j0 >= lo && j0 + 256 <= hi) return o;   // none is protected or past the end
+    const int j = j0 + 4 * lane;
+    auto mark = [&](int at, uint32_t& one) {
+      if (at < lo || at >= hi) one = at < n ? kProtected : 0;
+    };
+    mark(j, o.x), mark(j + 1, o.y), mark(j + 2, o.z), mark(j + 3, o.w);
+    return o;
+  };
   constexpr int kKept = HELD > 0 ? HELD : 1;
   float4 held[kKept];
+  uint4 held_orders[kKept];
   if (HELD > 0) {
 #pragma unroll
     for (int i = 0; i < kKept; ++i) held[i] = load4(w_lo + 256 * i + 4 * lane);
   }
-  auto each = [&](auto f) {   // f(first token of the lane's four, their usage)
+  for (int i = tid; i < kBins / 4; i += kSelThreads)
+    reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0, 0, 0, 0);
+  if (HELD > 0) {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) held_orders[i] = orders(w_lo + 256 * i, held[i]);
+  }
+  __syncthreads();
+  auto each = [&](auto f) {   // f(first token of the lane's four, their orders, their usage)
     if (HELD > 0) {
 #pragma unroll
       for (int i = 0; i < kKept; ++i)
-        if (i < steps) f(w_lo + 256 * i + 4 * lane, held[i]);
+        if (i < steps) f(w_lo + 256 * i + 4 * lane, held_orders[i], held[i]);
     } else {
-      for (int i = 0; i < steps; ++i) {
-        const int j = w_lo + 256 * i + 4 * lane;
-        f(j, load4(j));
+      constexpr int kAtOnce = 4;   // loads in flight
+      for (int i0 = 0; i0 < steps; i0 += kAtOnce) {
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) v[i] = load4(w_lo + 256 * (i0 + i) + 4 * lane);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int j0 = w_lo + 256 * (i0 + i);
+          if (i0 + i < steps) f(j0 + 4 * lane, orders(j0, v[i]), v[i]);
+        }
       }
     }
   };
 
   // -------- T, bits from the top, and r
-  uint32_t prefix = 0;
   int left = a.budget - a.sinks - a.recent;   // how many of the values that begin with the prefix are kept
+  uint32_t T = kTop;                          // (left == 0: none is above it, and none of those equal to it is kept)
+  uint32_t prefix = 0;
+#pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
-    uint4* const zero = reinterpret_cast<uint4*>(sh.counts);
-    for (int i = tid; i < kBins / 4; i += kSelThreads) zero[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    each([&](int j, const float4& four) {
-      const uint32_t o[4] = {order_of(four.x), order_of(four.y), order_of(four.z), order_of(four.w)};
+    if (left == 0) break;
+    const int shift = pass == 0 ? 20 : (pass == 1 ? 10 : 0), bits = pass == 0 ? 12 : 10, bins = 1 << bits;
+    uint32_t* const counts = sh.counts + (pass == 0 ? 0 : (pass == 1 ? 4096 : 4096 + 1024));
+    each([&](int, const uint4& four, const float4&) {
+      const uint32_t o[4] = {four.x, four.y, four.z, four.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool in = j + e >= lo && j + e < min(hi, w_hi) &&
-                        (pass == 0 || o[e] >> (shift + (pass == 2 ? 10 : 11)) == prefix);
+        const bool in = pass == 0 || o[e] >> shift >> bits == prefix;
         const uint32_t bin = (o[e] >> shift) & (bins - 1);
         const uint64_t who = __ballot(in);
         if (who == 0) continue;
@@ -88,21 +120,20 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
         const int lead = __ffsll((unsigned long long)who) - 1;
         const uint32_t one = (uint32_t)__builtin_amdgcn_readlane((int)bin, lead);
         if (__ballot(in && bin != one) == 0) {
-          if (lane == lead) atomicAdd(&sh.counts[one], (uint32_t)__popcll(who));
+          if (lane == lead) atomicAdd(&counts[one], (uint32_t)__popcll(who));
         } else if (in) {
-          atomicAdd(&sh.counts[bin], 1u);
+          atomicAdd(&counts[bin], 1u);
         }
       }
     });
     __syncthreads();
-    // the bin that holds the left-th largest: bins from the top, two a thread
-    const int b1 = bins - 1 - 2 * tid, b0 = b1 - 1;
-    int c1 = 0, c0 = 0;
-    if (b1 > 0) {
-      c1 = (int)sh.counts[b1];
-      c0 = (int)sh.counts[b0];
-    }
-    int incl = c1 + c0;
+    // the bin that holds the left-th largest: bins from the top, four a thread (the protected ones' is left out)
+    const int low = bins - 4 * (tid + 1);
+    uint4 c = make_uint4(0, 0, 0, 0);
+    if (low >= 0) c = *reinterpret_cast<const uint4*>(counts + low);
+    if (pass == 0 && tid == 0) c.w = 0;
+    const int c4[4] = {(int)c.w, (int)c.z, (int)c.y, (int)c.x}, sum = c4[0] + c4[1] + c4[2] + c4[3];
+    int incl = sum;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(incl, d, 64);
@@ -110,40 +141,41 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
     }
     if (lane == 63) sh.wave_sum[wave] = incl;
     __syncthreads();
-    int above = incl - c1 - c0;
+    int above = incl - sum;
 #pragma unroll
     for (int k = 0; k < kSelWaves; ++k) above += k < wave ? sh.wave_sum[k] : 0;
-    if (b1 > 0) {
-      if (left > above && left <= above + c1) {
-        sh.found_bin = b1;
-        sh.found_left = left - above;
-      } else if (left > above + c1 && left <= above + c1 + c0) {
-        sh.found_bin = b0;
-        sh.found_left = left - above - c1;
+    if (left > above && left <= above + sum) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (left > above && left <= above + c4[e]) {
+          sh.found_bin = low + 3 - e;
+          sh.found_left = left - above;
+          sh.found_count = c4[e];
+        }
+        above += c4[e];
       }
     }
-    if (left == 0 && tid == 0) {   // none is chosen: the largest order there is, and none of it
-      sh.found_bin = bins - 1;
-      sh.found_left = 0;
-    }
     __syncthreads();
-    prefix = prefix << (pass == 2 ? 10 : 11) | (uint32_t)sh.found_bin;
+    prefix = prefix << bits | (uint32_t)sh.found_bin;
     left = sh.found_left;
+    T = prefix << shift;
+    if (pass < 2 && left == sh.found_count && T > 0) {   // all values of this prefix are kept: the rest of their bits is not needed
+      T -= 1;
+      left = 0;
+    }
   }
-  const uint32_t T = prefix;
 
   // -------- the places of the kept: tokens before a lane's e-th are those of all lanes before it and its own e
   struct Marks {
     uint64_t above[4], equal[4];   // lanes whose e-th token is protected or above T, or equal to it
   };
-  auto look = [&](int j, const float4& four) {
-    const uint32_t o[4] = {order_of(four.x), order_of(four.y), order_of(four.z), order_of(four.w)};
+  auto look = [&](const uint4& four) {
+    const uint32_t o[4] = {four.x, four.y, four.z, four.w};
     Marks m;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bool in = j + e < w_hi, safe = j + e < lo || j + e >= hi;
-      m.above[e] = __ballot(in && (safe || o[e] > T));
-      m.equal[e] = __ballot(in && !safe && o[e] == T);
+      m.above[e] = __ballot(o[e] > T);
+      m.equal[e] = __ballot(o[e] == T);
     }
     return m;
   };
@@ -156,8 +188,8 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
     return n;
   };
   int n_above = 0, n_equal = 0;
-  each([&](int j, const float4& four) {
-    const Marks m = look(j, four);
+  each([&](int, const uint4& four, const float4&) {
+    const Marks m = look(four);
     n_above += all_of(m.above);
     n_equal += all_of(m.equal);
   });
@@ -173,9 +205,9 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
     n_above += k < wave ? sh.wave_sum[k] : 0;
     n_equal += k < wave ? sh.wave_eq[k] : 0;
   }
-  each([&](int j, const float4& four) {
-    const Marks m = look(j, four);
-    const float v[4] = {four.x, four.y, four.z, four.w};
+  each([&](int j, const uint4& four, const float4& usage4) {
+    const Marks m = look(four);
+    const float v[4] = {usage4.x, usage4.y, usage4.z, usage4.w};
     int at_a = n_above + before(m.above), at_e = n_equal + before(m.equal);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

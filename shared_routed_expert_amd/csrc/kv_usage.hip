@@ -3,16 +3,26 @@
 //   usage_j = decay prev_j + sum_{i, g} exp(z_{ig,j} - lse_{ig})     over the rows (i, g) that see key j,
 // from q, the cached keys and the attention call's own lse: the weights themselves are never stored.
 //
-// Keys stay, rows pass. A workgroup's four waves hold KPW keys each in registers, as the A operand of 16x16x32 matrix
-// instructions, and the rows come by in tiles of 32 through LDS, one tile ahead. A lane of the result S = K Q^T owns one row
-// (its column l & 15) and 4 keys per 16, so a weight is one fma (score, scale, -lse), one exponential, and one fma into
-// the lane's own sum of that key; the 16 lanes of a key are added up once, after the last row. lse log2 e is split into
-// its float32 value and a factor 2^-remainder that rides in the last fma.
+// Two kernels by how many rows (token, head of the group) a sequence may have.
 //
-// Work split. A segment is one block of 4 KPW keys of a sequence and kv head against all rows that see one of them. All segments
-// are laid end to end, each as long as its rows and a fixed cost, and workgroup w takes the w-th of equal parts of that
-// line. A segment in several parts leaves one partial sum per part, added in part order by a second kernel (no atomics,
-// the same bits every time); calls of at most 32 rows per sequence never split one and have no second kernel.
+// More than 32: keys stay, rows pass. A workgroup's four waves hold 64 keys each in registers (32 at D = 256), as the A operand
+// of 32x32x16 matrix instructions, and the rows come by in tiles of 128 (64) through LDS, straight from global memory, one
+// tile ahead. A lane of the result S = K Q^T owns one row (its column l & 31) and 16 keys per 32, so a weight is one fma
+// (score, scale, -lse), one exponential, and one fma into the lane's own sum of that key; the 32 lanes of a key are added
+// up once, after the last row. lse log2 e is split into its float32 value and a factor 2^-remainder that rides in the last
+// fma. The weights of one 32 x 32 tile are computed between the products of the next one. (16x16x32 products took 41 and
+// 139 us in the two cases below instead of 38 and 126: twice the instructions for the same keys.)
+//   Work split. A segment is one block of the workgroup's keys of a sequence and kv head against all rows that see one of them.
+// All segments are laid end to end, each as long as its rows and a fixed cost, and workgroup w takes the w-th of 512 equal
+// parts of that line, two workgroups on a CU: one's vector work beside the other's products. A segment in several parts
+// leaves one partial sum per part, added in part order by a second kernel (no atomics, the same bits every time).
+//   What bounds it: the vector unit and the matrix cores in turn, 3 vector instructions for every weight against 2 D / 1024
+// matrix cycles. Two prompts of 4096 tokens behind 1904 cached ones, 12 heads of 128, take 121 us (822 TFLOP/s, matrix cores
+// 36% busy): 116 for this kernel, 4 for the sums. The last 64 tokens of 131072 cached in e4m3 34 us (755 TFLOP/s), of which
+// some 3 find the parts, 3 to 6 wait for the keys, 4 are the sums. One workgroup per CU with 128 keys a wave: 191 and 34.
+//
+// At most 32 (decoding): bound by the keys' bytes; see kv_usage_few_kernel. 64 single tokens over up to 8192 keys, 82 MB, take
+// 20 to 22 us (4.1 TB/s, a launch included).
 #include "kv_usage.hpp"
 #include "attention_common.hpp"
 

@@ -142,6 +142,35 @@ def test_values(kind):
             c.run(budget, 4, 9, in_place)
 
 
+@pytest.mark.parametrize("n", [61, 1001, 33001])
+@pytest.mark.parametrize("kind", ["leading bits", "more bits", "all NaN", "NaN and lowest", "no choice"])
+def test_whole_bins_kept(n, kind):
+    """The kept are all values that share their leading bits, or reach into the lowest there are, or are the protected alone."""
+    rng = np.random.default_rng(n)
+    few = n // 5
+    c = Cut([n], few + 4, 1, 64, 16, seed=n)
+    row = c.usage[0, 0]
+    row[:] = rng.uniform(0.001, 0.002, row.size)
+    chosen = rng.permutation(np.arange(1, n - 3))[:few]
+    if kind == "leading bits":      # one exponent, above the others
+        row[chosen] = rng.uniform(1.0, 1.1, few)
+    elif kind == "more bits":       # values that differ in their last ten bits alone
+        row[:] = 1.0
+        row[chosen] = (np.float32(1.5).view(np.uint32) + rng.integers(0, 1024, few).astype(np.uint32)).view(np.float32)
+    elif kind == "all NaN":
+        row[:] = np.nan
+    elif kind == "NaN and lowest":  # some NaN are kept, the earlier ones
+        row[:] = np.nan
+        row[chosen[:few // 2]] = np.where(np.arange(few // 2) % 2 == 0, -np.inf, -np.finfo(np.float32).max)
+    for in_place in (False, True):
+        if kind == "no choice":
+            c.run(few + 4, few, 4, in_place)
+        else:
+            c.run(few + 4, 1, 3, in_place)
+            if kind in ("leading bits", "more bits"):
+                assert set(c.d_kept[0, 0].tolist()) == {0, n - 3, n - 2, n - 1} | set(chosen.tolist())
+
+
 def test_negative_zero_is_zero():
     """-0 and 0 are equal: the earlier is kept."""
     c = Cut([100], 10, 1, 64, 16)
