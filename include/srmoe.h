@@ -495,7 +495,9 @@ size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, i
  *                it become zeros.
  *   new_lens     [S] int32 out: budget, or kv_lens[s] (at most max_pages * page_size) where nothing is cut
  *   kept         [S, num_kv_heads, budget] int32 out: the old places of the kept tokens, ascending
- *   new_usage    as usage, out: the kept tokens' usage in their new places 0 .. budget - 1; it may be usage itself.
+ *   new_usage    as usage, out: the kept tokens' usage in their new places 0 .. budget - 1; it may be usage itself. Two
+ *                sequences of one row that are both cut leave it undefined, and with new_usage = usage what they keep
+ *                as well (kept's entries then, too).
  *   Rows of sequences that are not cut, in kept, new_usage and the cache, keep what they hold, as do the places past budget.
  *   limits: those of the cache; 1 <= budget <= limit; sinks, recent >= 0, sinks + recent <= budget; S * num_kv_heads <=
  *   65535; max_pages * page_size < 2^30. new_lens is not kv_lens, new_table not block_table.

@@ -212,8 +212,9 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const bool up = (m.above[e] >> lane) & 1, eq = (m.equal[e] >> lane) & 1;
-      if (up || (eq && at_e < left)) {
-        const int to = at_a + min(at_e, left);
+      const int to = at_a + min(at_e, left);
+      // (never budget or more, unless another sequence of the same row writes it meanwhile)
+      if ((up || (eq && at_e < left)) && to < a.budget) {
         kept[to] = j + e;
         if (HELD > 0 && usage) out[to] = v[e];   // (out may be usage: nobody reads it any more)
       }
@@ -235,7 +236,7 @@ __device__ __forceinline__ void select(const EvictArgs& a, Select& sh, const flo
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = i0 + k * kSelThreads + tid;
-      if (i < a.budget) v[k] = usage[kept[i]];
+      if (i < a.budget) v[k] = usage[min((uint32_t)kept[i], (uint32_t)n - 1)];
     }
     __syncthreads();
 #pragma unroll
@@ -272,7 +273,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int kMoveThreads = 256, kMoveEach = 2;
 __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a, const int lanes /* of a row */) {
   const int s = blockIdx.y / a.Hkv, h = blockIdx.y % a.Hkv;
-  if (cached_tokens(a, s) <= a.limit) return;
+  const int n = cached_tokens(a, s);
+  if (n <= a.limit) return;
   const int32_t* const kept = a.kept + ((size_t)s * a.Hkv + h) * a.budget;
   const int at_once = kMoveThreads / lanes, lane = threadIdx.x % lanes;
   const int first = blockIdx.x * kMoveEach * at_once + threadIdx.x / lanes;
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
     go[x] = i < a.budget;
     k[x] = v[x] = i32x4{0, 0, 0, 0};
     if (!go[x]) continue;
-    const int j = kept[i];
+    const int j = (int)min((uint32_t)kept[i], (uint32_t)n - 1);
     const int src = a.block_table[(size_t)s * a.max_pages + (j >> a.page_shift)];
     const int dst = a.new_table[(size_t)s * a.new_max_pages + (i >> a.page_shift)];
     go[x] = dst >= 0 && dst < a.num_pages;

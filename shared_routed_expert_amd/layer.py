@@ -6,6 +6,7 @@ combine).
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import numpy as np
@@ -133,6 +134,16 @@ class FusedMoE:
                                           self.expert_offsets, self.num_padded, self.align_ws, self.align_ws_bytes,
                                           self.ws, self.ws_bytes, self.out, list(events), stream)
 
+    def _memory_of(self, stream):
+        """Where what a call allocates belongs to its stream: a freed tensor's memory is given out in the order of the
+        stream that it was allocated on."""
+        if stream is None:
+            return nullcontext()
+        if isinstance(stream, int):
+            dev = self.out.device
+            stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
+        return torch.cuda.stream(stream)
+
     def _router_ws(self):
         if not hasattr(self, "router_ws"):
             self.router_ws_bytes = L.moe_route_from_x_workspace_bytes(self.T, self.H, self.E)
@@ -166,10 +177,11 @@ class FusedMoE:
             raise ValueError(f"weight is float32 [{H}] on {self.out.device}")
         if self.out.device.type != "cuda":
             raise ValueError("the layer is not on a GPU")
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(residual)
-        if y is None:
-            y = torch.empty((T, H), dtype=torch.bfloat16, device=self.out.device)
+        with self._memory_of(stream):
+            if residual is not None and residual_out is None:
+                residual_out = torch.empty_like(residual)
+            if y is None:
+                y = torch.empty((T, H), dtype=torch.bfloat16, device=self.out.device)
         base = self.ws.data_ptr()
         with torch.cuda.device(self.out.device):
             L.moe_add_rms_norm(x, x.stride(0) if T > 1 else H, residual, residual_out, weight, eps, T, H, self.scale_mode, y,
@@ -191,7 +203,8 @@ class FusedMoE:
         """What stands behind the attention, whole: add_norm, the router gate and routing on y, and the layer on y's
         codes. Returns (out, residual_out)."""
         y, h = self.add_norm(x, norm_w, residual, eps, residual_out, stream=stream)
-        self._router_ws()
+        with self._memory_of(stream):
+            self._router_ws()
         with torch.cuda.device(self.out.device):
             L.moe_route_from_x(y, w_router, bias, self.T, self.H, self.E, self.K, shared_weight, self.topk_ids, self.topk_w,
                                self.router_ws, self.router_ws_bytes, stream)

@@ -210,3 +210,26 @@ def test_the_layer_behind_the_norm(cfg, bm):
     assert torch.equal(codes, other.ws_view("xq", torch.uint8, (T, H)))
     assert torch.equal(layer.topk_ids, other.topk_ids) and torch.equal(layer.topk_w, other.topk_w)
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_call_on_a_stream_allocates_there(raw):
+    """forward_normed on a stream that is behind: what it frees on returning is not given to the current stream's tensors."""
+    inp = generate(small_cfg("streams", T=64, H=384, I=96, E=12, K=3, seed=12))
+    layer, W = make_layer(inp, 16)
+    T, H = 64, 384
+    rng = np.random.default_rng(0)
+    x = bf16_dev(bf16_bits_from_f32(rng.standard_normal((T, H)).astype(np.float32)))
+    w, wr = up(np.ones(H, np.float32)), to_dev(inp.router_w)
+    want, h = layer.forward_normed(x, w, wr, None, W, residual=x)
+    want = want.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    note(f"norm on a stream behind, raw={raw}")
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got, other = layer.forward_normed(x, w, wr, None, W, residual=x, stream=side.cuda_stream if raw else side)
+    mine = [torch.zeros((T, H), dtype=torch.bfloat16, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in mine)
+    assert torch.equal(got, want) and torch.equal(other, h)

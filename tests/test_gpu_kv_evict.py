@@ -286,3 +286,21 @@ def test_cache_object():
     c.d_kept = torch.cat([kept, pad])
     c.d_lens = torch.cat([lens, torch.full((4,), GUARD, dtype=torch.int32, device=DEV)])
     c.check(True)
+
+
+@pytest.mark.parametrize("n", [3000, 40000])
+def test_two_sequences_of_one_row(n):
+    """What they keep is undefined where the row is compacted in place; nothing else is touched."""
+    class Twice(Cut):
+        def check(self, in_place):
+            assert self.d_lens.tolist() == [self.budget] * 2 + [n // 4] + [GUARD] * 4
+            kept = self.d_kept.cpu().numpy()
+            assert (kept[2:] == GUARD).all()
+            usage = self.d_usage.cpu().numpy()
+            assert np.array_equal(usage[0, :, n:], self.usage[0, :, n:]) and np.array_equal(usage[1], self.usage[1])
+            kv = self.d_kv.view(torch.uint8).cpu().numpy()
+            new = set(self.new_table[:2].ravel().tolist())
+            same = [p for p in range(len(kv)) if p not in new]
+            assert np.array_equal(kv[same], self.kv[same])
+            assert ((kept[:2] >= -1) & (kept[:2] < n) | (kept[:2] == GUARD)).all()
+    Twice([n, n, n // 4], n // 4, 2, 64, 64, fp8=True, seed=n, rows=[0, 0, 1], num_rows=2).run(n // 4, 4, 50)
