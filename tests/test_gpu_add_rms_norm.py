@@ -233,3 +233,30 @@ def test_a_call_on_a_stream_allocates_there(raw):
     torch.cuda.synchronize()
     assert not any(t.any() for t in mine)
     assert torch.equal(got, want) and torch.equal(other, h)
+
+
+def test_forward_normed_captured():
+    """Captured and replayed on new values, with eager calls of the same layer between the replays."""
+    inp = generate(small_cfg("captured", T=64, H=384, I=96, E=12, K=3, seed=12))
+    layer, W = make_layer(inp, 16)
+    T, H = 64, 384
+    rng = np.random.default_rng(1)
+    new = lambda: bf16_dev(bf16_bits_from_f32(rng.standard_normal((T, H)).astype(np.float32)))
+    x, r = new(), new()
+    w, wr = up(rng.uniform(0.5, 1.5, H).astype(np.float32)), to_dev(inp.router_w)
+    note("norm and layer captured")
+    layer.forward_normed(x, w, wr, None, W, residual=r)
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        out, h = layer.forward_normed(x, w, wr, None, W, residual=r)
+    for rep in range(4):
+        x.copy_(new())
+        r.copy_(new())
+        want, want_h = layer.forward_normed(x, w, wr, None, W, residual=r)
+        want, want_h = want.clone(), want_h.clone()
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(h, want_h), rep
