@@ -398,10 +398,17 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
       for (int t = 0; t < C::AT; ++t)
 #pragma unroll
         for (int e = 0; e < 16; ++e) sum[t][e] = 0.f;
-      auto step = [&](int t, auto masked) {
-        // this tile is there, and the other buffer's rows have been read
+      // tile t is there, and the other buffer's rows have been read
+      auto arrive = [&](int t) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (t + 1 < t1) fetch(t + 1, buf ^ 1);
+      };
+      auto leave = [&](int t) {
+        buf ^= 1;
+        if (t + 1 < t1) put_lse(t + 1, buf);
+      };
+      auto step = [&](int t, auto masked) {
+        arrive(t);
         const int first = r0 + t * C::ROWS, groups = (min(C::ROWS, r_end - first) + 31) >> 5;
         const uint16_t* const rows_q = qs + buf * (C::ROWS * D);
         bf16x8 q[C::STEPS];
@@ -473,11 +480,15 @@ kv_usage_kernel(const UsageArgs args, const uint64_t magic, const uint32_t magic
           for (int g = 0; g + 1 < groups; ++g) group(g, std::false_type{});
           group(groups - 1, std::true_type{});
         }
-        buf ^= 1;
-        if (t + 1 < t1) put_lse(t + 1, buf);
+        leave(t);
       };
-      // later rows see more: once a tile's first row sees every key of this wave, all that follow do
+      // later rows see more: tiles whose last row sees no key of this wave come first, and once a tile's first row sees every one,
+      // all that follow do
       int t = t0;
+      for (; t < t1 && max(seq.ctx + uni(token_of(min(r0 + (t + 1) * C::ROWS, r_end) - 1)), seq.all) < wk; ++t) {
+        arrive(t);
+        leave(t);
+      }
       for (; t < t1 && wk + C::KPW > max(seq.ctx + uni(token_of(r0 + t * C::ROWS)), seq.all) + 1; ++t) step(t, std::true_type{});
       for (; t < t1; ++t) step(t, std::false_type{});
       const float total_weight = column_sum32(sum[0], sum[C::AT - 1], lane);   // (every lane takes part)
