@@ -16,10 +16,10 @@
 // All segments are laid end to end, each as long as its rows and a fixed cost, and workgroup w takes the w-th of 512 equal
 // parts of that line, two workgroups on a CU: one's vector work beside the other's products. A segment in several parts
 // leaves one partial sum per part, added in part order by a second kernel (no atomics, the same bits every time).
-//   What bounds it: the vector unit and the matrix cores in turn, 3 vector instructions for every weight against 2 D / 1024
-// matrix cycles. Two prompts of 4096 tokens behind 1904 cached ones, 12 heads of 128, take 121 us (822 TFLOP/s, matrix cores
-// 36% busy): 116 for this kernel, 4 for the sums. The last 64 tokens of 131072 cached in e4m3 34 us (755 TFLOP/s), of which
-// some 3 find the parts, 3 to 6 wait for the keys, 4 are the sums. One workgroup per CU with 128 keys a wave: 191 and 34.
+//   What bounds it: the vector unit and the matrix cores in turn, 3 vector instructions for 64 weights against D / 8 cycles of
+// the matrix core. Two prompts of 4096 tokens behind 1904 cached ones, 12 heads of 128, take 116 to 120 us (840 TFLOP/s,
+// matrix cores 37% busy), 4 of them for the sums. The last 64 tokens of 131072 cached in e4m3 take 34 (755 TFLOP/s), of which
+// some 2 find the parts, 3 to 6 wait for the keys, 4 are the sums. One workgroup per CU with 128 keys a wave: 191 and 34.
 //
 // At most 32 (decoding): bound by the keys' bytes; see kv_usage_few_kernel. 64 single tokens over up to 8192 keys, 82 MB, take
 // 20 to 22 us (4.1 TB/s, a launch included).
