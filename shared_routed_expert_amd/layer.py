@@ -170,8 +170,9 @@ class FusedMoE:
         for t, name in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (y, "y")):
             if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, H) or t.device != self.out.device):
                 raise ValueError(f"{name} is bf16 [{T}, {H}] on {self.out.device}")
-            if t is not None and (t.stride(1) != 1 and H > 1 or t is not x and not t.is_contiguous()):
-                raise ValueError(f"{name} is contiguous" + (" in its rows" if t is x else ""))
+            # (only x's rows may be strided, also where another argument is x itself)
+            if t is not None and not (t.stride(1) == 1 or H == 1 if name == "x" else t.is_contiguous()):
+                raise ValueError(f"{name} is contiguous" + (" in its rows" if name == "x" else ""))
         if x is None or weight is None or weight.dtype != torch.float32 or tuple(weight.shape) != (H,) \
                 or not weight.is_contiguous() or weight.device != self.out.device:
             raise ValueError(f"weight is float32 [{H}] on {self.out.device}")
