@@ -346,10 +346,12 @@ int moe_rope_cos_sin_table(float* cos_sin, int max_pos, int rotary_dim, double t
  * moe_ffn_quant_x ahead of moe_ffn_experts, or of moe_ffn_gate_up + moe_ffn_down, one pass over x and one rounding to
  * bf16 fewer (the codes are of y itself, not of its bf16 value).
  *   x            rows of H bf16 values, x_stride values apart (>= H, a multiple of 8)
- *   residual     [T,H] bf16, or NULL: none (h = x);  residual_out [T,H] bf16, or NULL. It may be residual itself.
- *   weight       [H] float32;  y [T,H] bf16, or NULL (it may be x where x_stride == H)
+ *   residual     [T,H] bf16, or NULL: none (h = x);  residual_out [T,H] bf16, or NULL
+ *   weight       [H] float32;  y [T,H] bf16, or NULL
  *   xq           [T,H] e4m3, or NULL (then sx is NULL and scale_mode is not used): y or xq is given
- * No other output overlaps an input. Sums and scales are float32 (h^2 up to 2^127); a NaN or an infinity stays in its row.
+ * residual_out and y may each be residual itself, or x itself where x_stride == H (or T == 1). Any other overlap of an
+ * output with another tensor of the call is refused. Sums and scales are float32 (h^2 up to 2^127); a NaN or an infinity
+ * stays in its row.
  *   limits: H % 8 == 0 (block scales: H % 128 == 0), H <= 65536, 0 <= eps < 1e30.
  * ------------------------------------------------------------------------- */
 int moe_add_rms_norm(const uint16_t* x, size_t x_stride, const uint16_t* residual, uint16_t* residual_out,

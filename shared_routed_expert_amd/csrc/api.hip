@@ -745,6 +745,14 @@ int moe_qk_norm_rope(uint16_t* qkv, int T, int num_q_heads, int num_kv_heads, in
                                         as_stream(stream)));
 }
 
+// Does a range of bytes touch any of T rows of `row` bytes, `stride` bytes apart? (No pointer: no.)
+static bool touches(const void* range, size_t bytes, const void* rows, size_t row, size_t stride, int T) {
+  if (!range || !rows) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(range), s = reinterpret_cast<uintptr_t>(rows);
+  const uintptr_t k = a < s + row ? 0 : (a - s - row) / stride + 1;   // the first row that ends behind a
+  return k < (uintptr_t)T && s + k * stride < a + bytes;
+}
+
 int moe_add_rms_norm(const uint16_t* x, size_t x_stride, const uint16_t* residual, uint16_t* residual_out,
                      const float* weight, float eps, int T, int H, int scale_mode, uint16_t* y, uint8_t* xq, float* sx,
                      void* stream) {
@@ -758,6 +766,23 @@ int moe_add_rms_norm(const uint16_t* x, size_t x_stride, const uint16_t* residua
   const void* ptrs[] = {x, residual, residual_out, weight, y, xq, sx};
   for (const void* p : ptrs)
     if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
+  // Rows are read and written by different workgroups: an output is another array than the rest, or its rows are x's or the residual's.
+  const size_t bf16 = (size_t)T * H * 2, groups = scale_mode == SRMOE_SCALE_BLOCK128 ? H / kGroup : 1;
+  const struct {
+    const void* p;
+    size_t bytes;
+  } outs[] = {{residual_out, bf16}, {y, bf16}, {xq, bf16 / 2}, {sx, (size_t)T * groups * 4}};
+  for (int i = 0; i < 4; ++i) {
+    const bool rows = i < 2;
+    if (!(rows && outs[i].p == x && (T == 1 || x_stride == (size_t)H)) &&
+        touches(outs[i].p, outs[i].bytes, x, (size_t)H * 2, x_stride * 2, T))
+      return SRMOE_ERR_INVALID_ARG;
+    if (!(rows && outs[i].p == residual) && touches(outs[i].p, outs[i].bytes, residual, bf16, bf16, 1))
+      return SRMOE_ERR_INVALID_ARG;
+    if (touches(outs[i].p, outs[i].bytes, weight, (size_t)H * 4, (size_t)H * 4, 1)) return SRMOE_ERR_INVALID_ARG;
+    for (int k = 0; k < i; ++k)
+      if (touches(outs[i].p, outs[i].bytes, outs[k].p, outs[k].bytes, outs[k].bytes, 1)) return SRMOE_ERR_INVALID_ARG;
+  }
   NormArgs a{};
   a.x = x; a.x_stride = x_stride; a.residual = residual; a.residual_out = residual_out; a.weight = weight; a.eps = eps;
   a.T = T; a.H = H; a.block = scale_mode == SRMOE_SCALE_BLOCK128; a.y = y; a.xq = xq; a.sx = sx;

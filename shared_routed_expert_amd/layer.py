@@ -165,7 +165,7 @@ class FusedMoE:
         """moe_add_rms_norm in front of the layer: h = x + residual (x alone without one), y = its root-mean-square norm
         times weight [H] float32. Returns (y, h) in bf16 (h: None without a residual, unless residual_out is given) and leaves
         y's codes and scales in the workspace, where experts_normed finds them. x [T, H] bf16, rows may be
-        strided."""
+        strided. residual_out and y may each be residual, or an x of dense rows; the library refuses other overlaps."""
         T, H = self.T, self.H
         for t, name in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (y, "y")):
             if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, H) or t.device != self.out.device):

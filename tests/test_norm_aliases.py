@@ -33,3 +33,40 @@ def test_the_whole_block_behind_the_attention(name):
     m, w, x = layer(), torch.ones(H), wide()
     with pytest.raises(ValueError, match=f"{name} is contiguous"):
         m.forward_normed(x, w, None, None, None, **{name: x})
+
+
+# Bases of 2 MiB each that no call touches: every refusal comes before a launch.
+X, R, RO, W, Y, XQ, SX = (0x1000000 + 0x200000 * i for i in range(7))
+INVALID = -1
+
+
+def norm(**kw):
+    from shared_routed_expert_amd import _lib as L
+    a = dict(x=X, x_stride=H, residual=R, residual_out=RO, weight=W, eps=1e-5, T=T, H=H, scale_mode=0, y=Y, xq=XQ, sx=SX)
+    a.update(kw)
+    return L.moe_add_rms_norm(**a, stream=0, check=False)
+
+
+def test_rejects_outputs_that_are_x_where_its_rows_are_strided():
+    for kw in (dict(y=X), dict(residual_out=X), dict(y=X, residual_out=R), dict(y=X, residual=None, residual_out=None)):
+        assert norm(x_stride=2 * H, **kw) == INVALID, kw
+
+
+def test_rejects_outputs_that_overlap():
+    row, size = 2 * H, 2 * T * H
+    one = dict(xq=None, sx=None)
+    for kw in (dict(y=RO), dict(y=R, residual_out=R), dict(y=X, residual_out=X),                 # the same for both
+               dict(y=RO + row), dict(residual_out=Y + size - 16),                               # a part of one another
+               dict(y=X + row), dict(y=X - row), dict(residual_out=X + size - 16), dict(residual_out=R + 16),
+               dict(y=R - size + 16, **one), dict(y=X + row, x_stride=3 * H), dict(y=X + 5 * row, x_stride=2 * H),
+               dict(y=W), dict(residual_out=W + 4 * H - 16), dict(xq=X), dict(xq=X + size - 16), dict(xq=R), dict(xq=Y),
+               dict(xq=RO + 16), dict(xq=W), dict(sx=W), dict(sx=X + 16), dict(sx=R), dict(sx=Y), dict(sx=RO),
+               dict(sx=XQ + T * H - 16), dict(xq=SX), dict(sx=XQ - 16, scale_mode=1)):
+        assert norm(**kw) == INVALID, kw
+
+
+def test_pointers_apart_are_still_looked_at():
+    for name in ("x", "residual", "residual_out", "weight", "y", "xq", "sx"):
+        assert norm(**{name: 0x10000 + 4}) == INVALID, name
+    for kw in (dict(x=None), dict(weight=None), dict(xq=None), dict(sx=None), dict(y=None, xq=None, sx=None)):
+        assert norm(**kw) == INVALID, kw
