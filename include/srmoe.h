@@ -483,7 +483,7 @@ size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, i
  *   Sequences without query tokens, rows of no sequence and tokens past kv_lens keep what usage holds. A token of a page
  *   outside the pool gets 0 from this call. Weights and sums are float32, in a fixed order (no atomics).
  *   workspace    >= moe_kv_usage_workspace_bytes(...); limits and other arguments as for moe_prefill_attention; 0 <=
- *                decay <= 1. usage overlaps no input but prev.
+ *                decay <= 1. usage overlaps no input but prev, and that one whole or not at all.
  *
  * moe_kv_evict: every sequence with kv_lens[s] > limit is cut to `budget` tokens, each kv head by its own usage: it keeps
  * the first `sinks`, the last `recent`, and of those between them the budget - sinks - recent of largest usage (equal
@@ -497,12 +497,12 @@ size_t moe_attention_workspace_bytes(int S, int T, int max_q, int num_q_heads, i
  *                it become zeros.
  *   new_lens     [S] int32 out: budget, or kv_lens[s] (at most max_pages * page_size) where nothing is cut
  *   kept         [S, num_kv_heads, budget] int32 out: the old places of the kept tokens, ascending
- *   new_usage    as usage, out: the kept tokens' usage in their new places 0 .. budget - 1; it may be usage itself. Two
- *                sequences of one row that are both cut leave it undefined, and with new_usage = usage what they keep
- *                as well (kept's entries then, too).
+ *   new_usage    as usage, out: the kept tokens' usage in their new places 0 .. budget - 1; it may be usage itself (a part of
+ *                it is refused). Two sequences of one row that are both cut leave it undefined, and with new_usage =
+ *                usage what they keep as well (kept's entries then, too).
  *   Rows of sequences that are not cut, in kept, new_usage and the cache, keep what they hold, as do the places past budget.
  *   limits: those of the cache; 1 <= budget <= limit; sinks, recent >= 0, sinks + recent <= budget; S * num_kv_heads <=
- *   65535; max_pages * page_size < 2^30. new_lens is not kv_lens, new_table not block_table.
+ *   65535; max_pages * page_size < 2^30. new_lens does not overlap kv_lens, new_table is not block_table.
  * The cut leaves keys at the positions that they were rotated to; what comes next is appended behind the budget with its
  * own position.
  * ------------------------------------------------------------------------- */

@@ -74,6 +74,13 @@ constexpr int kMaxNoAllocDevices = 64;
 
 inline size_t al256(size_t n) { return (n + 255) / 256 * 256; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Does a range of bytes touch any of T rows of `row` bytes, `stride` bytes apart? (No pointer: no.)
+inline bool touches(const void* range, size_t bytes, const void* rows, size_t row, size_t stride, int T) {
+  if (!range || !rows) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(range), s = reinterpret_cast<uintptr_t>(rows);
+  const uintptr_t k = a < s + row ? 0 : (a - s - row) / stride + 1;   // the first row that ends behind a
+  return k < (uintptr_t)T && s + k * stride < a + bytes;
+}
 inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 int hip_status(hipError_t e) {
@@ -745,14 +752,6 @@ int moe_qk_norm_rope(uint16_t* qkv, int T, int num_q_heads, int num_kv_heads, in
                                         as_stream(stream)));
 }
 
-// Does a range of bytes touch any of T rows of `row` bytes, `stride` bytes apart? (No pointer: no.)
-static bool touches(const void* range, size_t bytes, const void* rows, size_t row, size_t stride, int T) {
-  if (!range || !rows) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(range), s = reinterpret_cast<uintptr_t>(rows);
-  const uintptr_t k = a < s + row ? 0 : (a - s - row) / stride + 1;   // the first row that ends behind a
-  return k < (uintptr_t)T && s + k * stride < a + bytes;
-}
-
 int moe_add_rms_norm(const uint16_t* x, size_t x_stride, const uint16_t* residual, uint16_t* residual_out,
                      const float* weight, float eps, int T, int H, int scale_mode, uint16_t* y, uint8_t* xq, float* sx,
                      void* stream) {
@@ -929,6 +928,12 @@ int moe_prefill_attention(const uint16_t* q, size_t q_stride, const void* k_cach
                    head_dim, scale, softcap, out, lse, workspace, ws_bytes, stream);
 }
 
+// Of [rows, kv heads, tokens of a table's row] float32; rows may be any number, so held to what an address can reach.
+static size_t usage_bytes(int rows, int num_kv_heads, int max_pages, int page_size) {
+  const size_t row = (size_t)num_kv_heads * max_pages * page_size * 4, most = (size_t)1 << 60;
+  return (size_t)rows < most / row ? rows * row : most;
+}
+
 size_t moe_kv_usage_workspace_bytes(int S, int T, int max_q, int num_q_heads, int num_kv_heads, int head_dim) {
   if (check_attention_dims(S, T, max_q, num_q_heads, num_kv_heads, head_dim) != SRMOE_OK) return 0;
   return kv_usage_workspace_bytes(head_dim);
@@ -952,6 +957,8 @@ int moe_kv_usage(const uint16_t* q, size_t q_stride, const void* k_cache, int kv
     if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_kv_usage_workspace_bytes(S, T, max_q, num_q_heads, num_kv_heads, head_dim))
     return SRMOE_ERR_WORKSPACE;
+  const size_t all = usage_bytes(rows, num_kv_heads, max_pages, page_size);
+  if (prev != usage && touches(usage, all, prev, all, all, 1)) return SRMOE_ERR_INVALID_ARG;
   UsageArgs u{};
   AttnArgs& a = u.a;
   a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.k_scale = kv_type == SRMOE_KV_E4M3 ? k_scale : nullptr;
@@ -981,7 +988,9 @@ int moe_kv_evict(void* k_cache, void* v_cache, int kv_type, int num_pages, int p
   if (S == 0) return SRMOE_OK;
   if (!k_cache || !v_cache || !block_table || !kv_lens || !usage || !new_usage || !new_table || !new_lens || !kept)
     return SRMOE_ERR_INVALID_ARG;
-  if (new_lens == kv_lens || new_table == block_table) return SRMOE_ERR_INVALID_ARG;
+  const size_t all = usage_bytes(rows, num_kv_heads, max_pages, page_size), lens = (size_t)S * 4;
+  if (touches(new_lens, lens, kv_lens, lens, lens, 1) || new_table == block_table) return SRMOE_ERR_INVALID_ARG;
+  if (new_usage != usage && touches(new_usage, all, usage, all, all, 1)) return SRMOE_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(new_table) & 3u) return SRMOE_ERR_INVALID_ARG;   // (a slice of a list of free pages)
   const void* ptrs[] = {k_cache, v_cache, block_table, kv_lens, usage, new_usage, usage_rows, new_lens, kept};
   for (const void* p : ptrs)
