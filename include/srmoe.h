@@ -350,8 +350,8 @@ int moe_rope_cos_sin_table(float* cos_sin, int max_pos, int rotary_dim, double t
  *   weight       [H] float32;  y [T,H] bf16, or NULL
  *   xq           [T,H] e4m3, or NULL (then sx is NULL and scale_mode is not used): y or xq is given
  * residual_out and y may each be residual itself, or x itself where x_stride == H (or T == 1). Any other overlap of an
- * output with another tensor of the call is refused. Sums and scales are float32 (h^2 up to 2^127); a NaN or an infinity
- * stays in its row.
+ * output with another tensor of the call is refused. Sums and scales are float32; rows whose h^2, its sum or h w leave
+ * float32's normal range are scaled first, so that any finite h gives its y. A NaN or an infinity stays in its row.
  *   limits: H % 8 == 0 (block scales: H % 128 == 0), H <= 65536, 0 <= eps < 1e30.
  * ------------------------------------------------------------------------- */
 int moe_add_rms_norm(const uint16_t* x, size_t x_stride, const uint16_t* residual, uint16_t* residual_out,
