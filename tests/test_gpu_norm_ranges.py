@@ -82,3 +82,20 @@ def test_nan_and_infinity_in_far_rows(H):
     assert np.all(np.isnan(y[[1, 2]])) and np.isnan(y[5, H - 1]) and np.isnan(y[6, 0])
     assert not np.any(y[5, :H - 1]) and not np.any(y[6, 1:])
     assert np.all(got[3][[1, 2, 5, 6]] == 1.0)
+
+
+@pytest.mark.parametrize("H", [8, 128, 384, 5120, 40000])
+def test_the_smallest_values(H):
+    """Subnormal bf16 values, eps = 0: multiples of 2^-133 up to 60 of them, whose sums are exact in bf16."""
+    rng = np.random.default_rng(H)
+    small = lambda: bf16_bits_from_f32((rng.integers(-60, 61, (5, H)) * 2.0 ** -133).astype(np.float32))
+    x, r = small(), small()
+    x[:, 0], r[:, 0] = bf16_bits_from_f32(np.float32([2.0 ** -133]))[0], 0   # (no row of zeros)
+    w = rng.uniform(-1.5, 1.5, H).astype(np.float32)
+    for mode, q in ((0, False), (0, True), (1, True)):
+        if mode and H % 128:
+            continue
+        note(f"norm of subnormal values H={H} mode={mode} codes={q}")
+        got = run(x, r, w, 0.0, H, mode, q=q)
+        check(x, r, w, 0.0, H, mode, got)
+        assert np.array_equal(values(got[0].view(np.uint16)), values(x) + values(r))
