@@ -145,6 +145,35 @@ __device__ __forceinline__ SeqTiles<WIN> uniform(SeqTiles<WIN> t) {
   return t;
 }
 
+template <bool WIN>
+__device__ __forceinline__ SeqTiles<WIN> lane_of(const SeqTiles<WIN>& t, int lane) {
+  SeqTiles<WIN> u;
+  u.row0 = __builtin_amdgcn_readlane(t.row0, lane);
+  u.n = __builtin_amdgcn_readlane(t.n, lane);
+  u.kv = __builtin_amdgcn_readlane(t.kv, lane);
+  u.ctx = __builtin_amdgcn_readlane(t.ctx, lane);
+  u.lo = __builtin_amdgcn_readlane(t.lo, lane);
+  u.MT = __builtin_amdgcn_readlane(t.MT, lane);
+  u.hi = __builtin_amdgcn_readlane(t.hi, lane);
+  return u;
+}
+// The next sequence with query tokens, looked for 64 at a time; false where there is none. (One by one, each waits for the last
+// one's lengths: 2 active sequences of 8192, one token each, under a window 1000 us instead of 55, causal 1255 and 58.)
+template <int NK, bool WIN>
+__device__ __forceinline__ bool next_seq(const AttnArgs& a, int TB, int& s, SeqTiles<WIN>& seq) {
+  for (int at = s + 1; at < a.S; at += 64) {
+    const SeqTiles<WIN> t = seq_tiles<NK, WIN>(a, min(at + (int)(threadIdx.x & 63), a.S - 1), TB);   // (the last one again past it)
+    const uint64_t some = __ballot(t.n > 0);
+    if (some) {
+      const int first = __ffsll((unsigned long long)some) - 1;
+      s = at + first;
+      seq = lane_of(t, first);
+      return true;
+    }
+  }
+  return false;
+}
+
 // How the segments are shared out: equal parts of the line, whole segments, or either by the lengths that the
 // kernel finds (a launch of both: as many workgroups as there can be segments, and the join).
 enum Share { kEqualParts, kWholeSegments, kByLengths };
@@ -297,13 +326,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 || KW == 8 ? 2 : 1, RW == 4 || KW == 
   if (few) {
     s = __ffsll((unsigned long long)__ballot(here)) - 1;
     rem = u - read_lane(before, s);
-    seq.row0 = __builtin_amdgcn_readlane(own.row0, s);
-    seq.n = __builtin_amdgcn_readlane(own.n, s);
-    seq.kv = __builtin_amdgcn_readlane(own.kv, s);
-    seq.ctx = __builtin_amdgcn_readlane(own.ctx, s);
-    seq.lo = __builtin_amdgcn_readlane(own.lo, s);
-    seq.MT = __builtin_amdgcn_readlane(own.MT, s);
-    seq.hi = __builtin_amdgcn_readlane(own.hi, s);
+    seq = lane_of(own, s);
   } else {
     if (here) {
       long r = u - before;
@@ -838,8 +861,7 @@ __attribute__((amdgpu_waves_per_eu(RW == 4 || KW == 8 ? 2 : 1, RW == 4 || KW == 
       mt = 0;
       if (++h >= a.Hkv && u < u_end) {
         h = 0;
-        do seq = uniform(seq_tiles<NK, WIN>(a, ++s, TB));
-        while (seq.n == 0);
+        if (!next_seq<NK, WIN>(a, TB, s, seq)) return;
       }
     }
   }

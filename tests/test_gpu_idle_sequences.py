@@ -1,9 +1,12 @@
 """A few sequences with query tokens among thousands without: runs of idle ones at the start, between and at the end, longer and
-shorter than a wavefront's 64 and on its borders; usage against its oracle."""
+shorter than a wavefront's 64 and on its borders; usage and the attention calls against their oracles."""
 import pytest
 
+import oracle
 from tests.kv_util import make_case
+from tests.test_gpu_attention import run_check as check_attention
 from tests.test_gpu_kv_usage import run_check as check_usage
+from tests.test_gpu_window_attention import run_check as check_window
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +37,17 @@ def test_usage_of_active_sequences_without_cached_tokens(n):
     for s in (70, 400):
         kvs[s] = 0
     check_usage(make_case(c.ns, kvs, 4, 1, 64, 16, False, seed=n), prev=True)
+
+
+@pytest.mark.parametrize("n", [1, 7, 20, 150])
+@pytest.mark.parametrize("S,places", [(65, [0, 64]), (200, [3, 199]), (4000, GAPS), (4500, GAPS + [4499]), (5000, [0, 4999]),
+                                      (5000, [4990, 4995, 4999])])
+def test_attention(S, places, n):
+    for fp8 in (False, True):
+        for wide in (False, True):
+            c = case(S, places, n, n + 300, fp8)
+            check_attention(c, "prefill", None, [oracle.visible_prefill(a, k, 0) for a, k in zip(c.ns, c.kvs)], wide=wide)
+            check_window(case(S, places, n, n + 300, fp8), 190, 5, wide=wide)
+        if n <= 64:
+            c = case(S, places, n, n + 300, fp8)
+            check_attention(c, "tree", None, [oracle.visible_tree(a, k, None) for a, k in zip(c.ns, c.kvs)])
