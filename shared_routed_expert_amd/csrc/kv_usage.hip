@@ -17,12 +17,14 @@
 // parts of that line, two workgroups on a CU: one's vector work beside the other's products. A segment in several parts
 // leaves one partial sum per part, added in part order by a second kernel (no atomics, the same bits every time).
 //   What bounds it: the vector unit and the matrix cores in turn, 3 vector instructions for 64 weights against D / 8 cycles of
-// the matrix core. Two prompts of 4096 tokens behind 1904 cached ones, 12 heads of 128, take 116 to 120 us (840 TFLOP/s,
-// matrix cores 37% busy), 4 of them for the sums. The last 64 tokens of 131072 cached in e4m3 take 34 (755 TFLOP/s), of which
-// some 2 find the parts, 3 to 6 wait for the keys, 4 are the sums. One workgroup per CU with 128 keys a wave: 191 and 34.
+// the matrix core. Two prompts of 4096 tokens behind 1904 cached ones, 12 heads of 128, take 116 to 126 us by the card (790
+// to 860 TFLOP/s, matrix cores 37% busy), 4 of them for the sums, with a cap of 30 174, of 100 221. The last 64 tokens of
+// 131072 cached in e4m3 take 34 to 37 (700 to 755 TFLOP/s), of which some 2 find the parts, 3 to 6 wait for the keys, 4 are
+// the sums. One workgroup per CU with 128 keys a wave: 191 and 34. At D = 256 a wave holds one tile of 32 keys, so its weights
+// have no products beside them: two prompts of 4096 after 1904, 8 heads, 154 to 160 us (830 to 860 TFLOP/s).
 //
 // At most 32 (decoding): bound by the keys' bytes; see kv_usage_few_kernel. 64 single tokens over up to 8192 keys, 82 MB, take
-// 20 to 22 us (4.1 TB/s, a launch included).
+// 20 to 22 us (3.7 to 4.1 TB/s, a launch included), 43 MB in e4m3 15, 162 MB of 8 heads of 256 30 to 32.
 #include "kv_usage.hpp"
 #include "attention_common.hpp"
 
