@@ -434,7 +434,7 @@ int moe_kv_append(const uint16_t* qkv, size_t qkv_stride, int T, int num_q_heads
  *   The cap adds a rounding of 2^-19 of the capped score, and of 2^-22 of a softcap up to 64.
  *   limits: those of the cache; num_q_heads a multiple of num_kv_heads, at most 128 times
  *   it, num_q_heads <= 1024; S <= 65536; max_pages * page_size < 2^30; 0 < scale <= 1e6;
- *   softcap 0 or in 1e-6..1e6. out and lse overlap no input.
+ *   softcap 0 or in 1e-6..1e6. out and lse overlap no input (q: refused).
  * Results do not depend on scheduling: no atomics, sums in a fixed order. That order goes by the call's sizes (S, T,
  * max_q, max_pages * page_size) and its sequences' lengths, so a sequence's last bits may differ between batches. */
 int moe_tree_attention(const uint16_t* q, size_t q_stride, const void* k_cache, const void* v_cache, int kv_type,

@@ -137,7 +137,7 @@ class PagedKVCache:
         """Attention of each sequence's last tokens (drafted ones: tree_mask [T] int64 words, bit b = the sequence's
         drafted token b is seen; None: a chain, with one token per sequence ordinary decoding) over its cached tokens.
         scale: head_dim^-1/2 unless given. Returns out [T, q heads, head_dim]; rows outside every sequence and a
-        sequence's tokens past max_q are zero, or left as they were in an out (and lse) that is given."""
+        sequence's tokens past max_q are zero, or left as they were in an out (and lse) that is given. out is not q."""
         if tree_mask is not None:
             self._tensor(tree_mask, "tree_mask", torch.int64, (q.shape[0],))
         return self._attention(L.moe_tree_attention, q, block_table, cu_q, kv_lens, (tree_mask,), max_q, scale, softcap,

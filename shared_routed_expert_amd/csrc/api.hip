@@ -893,6 +893,11 @@ static int attention(const uint16_t* q, size_t q_stride, const void* k_cache, co
     if (!aligned16(p)) return SRMOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_attention_workspace_bytes(S, T, max_q, num_q_heads, num_kv_heads, head_dim))
     return SRMOE_ERR_WORKSPACE;
+  // (a part of a segment may read q after another one has written the result)
+  const size_t row = (size_t)num_q_heads * head_dim * 2, all = T * row, stats = (size_t)T * num_q_heads * 4;
+  if (touches(out, all, q, row, q_stride * 2, T) || touches(lse, stats, q, row, q_stride * 2, T) ||
+      touches(lse, stats, out, all, all, 1))
+    return SRMOE_ERR_INVALID_ARG;
   AttnArgs a{};
   a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache;
   a.k_scale = kv_type == SRMOE_KV_E4M3 ? k_scale : nullptr;
